@@ -32,6 +32,9 @@ __all__ = [
     "PACE_COMMIT_MMA", "PACE_COMMIT_TCGEN05", "pace_debug_wait_fault",
     "pace_quantize", "pace_dequantize", "pace_pool_status", "pace_pool_clear_status",
     "pace_gdn_step_f32", "pace_gdn_step_bf16", "pace_status_string", "pace_version",
+    "PACE_NORM_L2", "PACE_NORM_RMS", "pace_linattn_workspace_bytes", "pace_linattn_forward",
+    "pace_linattn_backward", "pace_linattn_step", "pace_qk_norm_workspace_bytes", "pace_qk_norm_rotate",
+    "pace_qk_norm_rotate_backward",
     "PacePool",
 ]
 
@@ -46,6 +49,7 @@ PACE_FLAG_TIMEOUT = 0x8
 PACE_FILL_COMMIT = 0x100
 PACE_WINDOW_STATIC_SCRATCH_BYTES = 8 << 20
 PACE_COMMIT_MMA, PACE_COMMIT_TCGEN05 = 0, 1
+PACE_NORM_L2, PACE_NORM_RMS = 0, 1
 PACE_OK, PACE_ERR_INVALID_ARG, PACE_ERR_UNSUPPORTED, PACE_ERR_CUDA, PACE_ERR_DEVICE_FLAGS = 0, 1, 2, 3, 4
 
 
@@ -60,6 +64,23 @@ class _Desc(ctypes.Structure):
                 ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("period", ctypes.c_int32),
                 ("scale_axis", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
                 ("head_bits", ctypes.POINTER(ctypes.c_uint8)), ("buffer_e4m3", ctypes.c_int32)]
+
+
+class _LinattnDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int64), ("max_len", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("o_stride", ctypes.c_int64)]
+
+
+class _QkNormDesc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("num_q_heads", ctypes.c_int32),
+                ("num_k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("q_scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
 
 
 def _load():
@@ -97,6 +118,13 @@ def _load():
         "pace_dequantize": [P, U16p, I64, I32, I32, I32, I32, F32p, P],
         "pace_pool_status": [P, P, ctypes.POINTER(ctypes.c_uint32)],
         "pace_pool_clear_status": [P, P],
+        "pace_linattn_workspace_bytes": [ctypes.POINTER(_LinattnDesc), I32, Sp],
+        "pace_linattn_forward": [ctypes.POINTER(_LinattnDesc)] + [P] * 11,
+        "pace_linattn_backward": [ctypes.POINTER(_LinattnDesc)] + [P] * 15,
+        "pace_linattn_step": [ctypes.POINTER(_LinattnDesc)] + [P] * 7,
+        "pace_qk_norm_workspace_bytes": [ctypes.POINTER(_QkNormDesc), Sp],
+        "pace_qk_norm_rotate": [ctypes.POINTER(_QkNormDesc)] + [P] * 9,
+        "pace_qk_norm_rotate_backward": [ctypes.POINTER(_QkNormDesc)] + [P] * 14,
         "pace_gdn_step_f32": [F32p, P, P, P, P, P, I32, F32p, I64, I32, I32, P],
         "pace_gdn_step_bf16": [U16p, P, P, P, P, P, I32, F32p, I64, I32, I32, P],
     }
@@ -326,6 +354,329 @@ def pace_gdn_step_bf16(S, q, k, v, alpha, beta, io, o, n, d_k, d_v, stream=None)
     _check("pace_gdn_step_bf16", lib.pace_gdn_step_bf16(_ptr(S), _ptr(q), _ptr(k), _ptr(v),
                                                          _ptr(alpha), _ptr(beta), io, _ptr(o), n,
                                                          d_k, d_v, _stream(stream)))
+
+
+# ------------------------------------------------ linear attention, query/key norms
+#
+# These calls check shapes, types and devices (the C entry points see pointers
+# only), run on the device of their first tensor whichever device is current,
+# allocate the outputs and the workspace that are not given, and return the
+# outputs.  Token rows may lie apart (a part of a wider projection): the last
+# two dimensions are dense, the row stride is free.
+
+_IO_OF = {torch.bfloat16: PACE_IO_BF16, torch.float32: PACE_IO_F32}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(name: str, t: torch.Tensor, heads: int, d: int, like: torch.Tensor) -> Tuple[int, int]:
+    """(rows, row stride in elements) of [..., heads, d] token rows."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.device == like.device, f"{name}: a tensor on {like.device}")
+    _need(t.dtype == like.dtype, f"{name}: {like.dtype}, not {t.dtype}")
+    sh, st = t.shape, t.stride()
+    _need(len(sh) >= 3 and sh[-1] == d and sh[-2] == heads, f"{name}: [..., {heads}, {d}] rows, not {tuple(sh)}")
+    rows = 1
+    for x in sh[:-2]:
+        rows *= x
+    if rows * heads == 0:
+        return rows, 0
+    _need((d == 1 or st[-1] == 1) and (heads == 1 or st[-2] == d), f"{name}: each row's heads are contiguous")
+    at = None                                   # the row stride; leading dimensions fold into one
+    for x, s in zip(reversed(sh[:-2]), reversed(st[:-2])):
+        if x == 1:
+            continue
+        if at is None:
+            at, span = s, s * x
+        else:
+            _need(s == span, f"{name}: the leading dimensions lie at one stride")
+            span = s * x
+    _need(at is None or at >= heads * d, f"{name}: rows that do not overlap")
+    return rows, 0 if at is None else at
+
+
+def _plain(name: str, t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor) -> Optional[int]:
+    """Address of an optional contiguous tensor of that shape and type on the device of `like`."""
+    if t is None:
+        return None
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.device == like.device, f"{name}: a tensor on {like.device}")
+    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+          f"{name}: contiguous {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+class _On:
+    """Makes a tensor's device current for a call and gives the stream to launch on."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.index = t.device.index
+        self.stream = stream
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.back != self.index:
+            torch.cuda.set_device(self.index)
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.back != self.index:
+            torch.cuda.set_device(self.back)
+        return False
+
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output or workspace for work on `stream` (None: the current one) of the device of `like`."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), like.device)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _workspace(name: str, nbytes: int, given: Optional[torch.Tensor], like: torch.Tensor, stream):
+    if given is None:
+        return _new(nbytes, torch.uint8, like, stream) if nbytes else None
+    _need(given.is_cuda and given.device == like.device and given.is_contiguous(), f"{name}: workspace on {like.device}")
+    _need(given.numel() * given.element_size() >= nbytes, f"{name}: workspace of {nbytes} bytes")
+    return given
+
+
+def _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens):
+    """Descriptor and common checks; (desc, rows of q, N, H, d)."""
+    _need(isinstance(q, torch.Tensor) and q.is_cuda, "libpace takes device tensors")
+    _need(q.dtype in _IO_OF, f"q: bfloat16 or float32, not {q.dtype}")
+    _need(q.dim() in (3, 4), "q: [tokens, heads, d] or [sequences, tokens, heads, d]")
+    H, d = q.shape[-2], q.shape[-1]
+    total, qs = _rows("q", q, H, d, q)
+    tk, ks = _rows("k", k, H, d, q)
+    tv, vs = _rows("v", v, H, d, q)
+    _need(tk == total and tv == total, "q, k and v: as many rows each")
+    if cu_seqlens is not None:
+        n = cu_seqlens.numel() - 1
+        _need(num_seqs is None or num_seqs == n, "cu_seqlens: num_seqs + 1 entries")
+        _need(max_len is None or max_len >= 0, "max_len: not negative")
+        longest = total if max_len is None else int(max_len)
+    else:
+        n = int(num_seqs) if num_seqs is not None else (q.shape[0] if q.dim() == 4 else 1)
+        _need(n >= 1 and total % n == 0, "without cu_seqlens every sequence has as many rows")
+        longest = total // n
+        _need(max_len is None or max_len == longest, "max_len: rows / num_seqs without cu_seqlens")
+    _need(n >= 1, "one sequence at least")
+    desc = _LinattnDesc(n, H, d, d, _IO_OF[q.dtype], total, longest, qs, ks, vs, 0)
+    return desc, total, n, H, d
+
+
+def pace_linattn_workspace_bytes(num_seqs: int, num_heads: int, d: int, io: int, total_tokens: int, max_len: int,
+                                 backward: bool = False) -> int:
+    desc = _LinattnDesc(num_seqs, num_heads, d, d, io, total_tokens, max_len, 0, 0, 0, 0)
+    n = ctypes.c_size_t()
+    _check("pace_linattn_workspace_bytes", lib.pace_linattn_workspace_bytes(ctypes.byref(desc), int(backward),
+                                                                            ctypes.byref(n)))
+    return n.value
+
+
+def pace_linattn_forward(q, k, v, log_decay, o=None, ST=None, num_seqs=None, max_len=None, cu_seqlens=None, S0=None,
+                         workspace=None, flags=None, stream=None, need_ST=True):
+    """Linear attention with a fixed decay for each head over prompts: returns (o, ST).
+
+    q, k, v: [tokens, H, d] packed prompts (or [N, T, H, d]); log_decay: fp32 [H];
+    cu_seqlens: int32 [N + 1], or None for prompts of one length; S0, ST: fp32 [N, H, d, d].  Rows of no sequence
+    are left as they are (unset in an o made here).
+    """
+    desc, total, n, H, d = _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens)
+    if o is None:
+        o = _new(q.shape, q.dtype, q, stream)
+    to, desc.o_stride = _rows("o", o, H, d, q)
+    _need(to == total, "o: as many rows as q")
+    if ST is None and need_ST:
+        ST = _new((n, H, d, d), torch.float32, q, stream)
+    g = _plain("log_decay", log_decay, (H,), torch.float32, q)
+    cu = _plain("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, q)
+    s0 = _plain("S0", S0, (n, H, d, d), torch.float32, q)
+    st = _plain("ST", ST, (n, H, d, d), torch.float32, q)
+    fl = _plain("flags", flags, (1,), torch.int32, q)
+    size = ctypes.c_size_t()
+    _check("pace_linattn_forward", lib.pace_linattn_workspace_bytes(ctypes.byref(desc), 0, ctypes.byref(size)))
+    ws = _workspace("pace_linattn_forward", size.value, workspace, q, stream)
+    with _On(q, stream) as s:
+        _check("pace_linattn_forward", lib.pace_linattn_forward(
+            ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), g, cu, s0, o.data_ptr(), st,
+            None if ws is None else ws.data_ptr(), fl, s))
+    return o, ST
+
+
+def pace_linattn_backward(q, k, v, log_decay, d_o, dq=None, dk=None, dv=None, dS0=None, num_seqs=None, max_len=None,
+                          cu_seqlens=None, S0=None, dST=None, workspace=None, flags=None, stream=None, need_dS0=None):
+    """Gradients of pace_linattn_forward: returns (dq, dk, dv, dS0); dS0 is None unless S0 or need_dS0 is given.
+
+    dq, dk, dv have the row strides of q, k, v; those not given are made so (rows of no sequence are left unset).
+    """
+    desc, total, n, H, d = _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens)
+    to, desc.o_stride = _rows("d_o", d_o, H, d, q)
+    _need(to == total, "d_o: as many rows as q")
+    made = []
+    for name, given, like, stride in (("dq", dq, q, desc.q_stride), ("dk", dk, k, desc.k_stride),
+                                      ("dv", dv, v, desc.v_stride)):
+        if given is None:
+            if stride in (0, H * d):
+                given = _new(like.shape, like.dtype, q, stream)
+            else:
+                room = _new(max(total, 1) * stride, like.dtype, q, stream)
+                given = room.as_strided(like.shape, like.stride())
+        tg, sg = _rows(name, given, H, d, q)
+        _need(tg == total and (total <= 1 or (sg or H * d) == (stride or H * d)), f"{name}: rows as those of {name[1:]}")
+        made.append(given)
+    dq, dk, dv = made
+    if dS0 is None and (S0 is not None if need_dS0 is None else need_dS0):
+        dS0 = _new((n, H, d, d), torch.float32, q, stream)
+    g = _plain("log_decay", log_decay, (H,), torch.float32, q)
+    cu = _plain("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, q)
+    s0 = _plain("S0", S0, (n, H, d, d), torch.float32, q)
+    dst = _plain("dST", dST, (n, H, d, d), torch.float32, q)
+    ds0 = _plain("dS0", dS0, (n, H, d, d), torch.float32, q)
+    fl = _plain("flags", flags, (1,), torch.int32, q)
+    size = ctypes.c_size_t()
+    _check("pace_linattn_backward", lib.pace_linattn_workspace_bytes(ctypes.byref(desc), 1, ctypes.byref(size)))
+    ws = _workspace("pace_linattn_backward", size.value, workspace, q, stream)
+    with _On(q, stream) as s:
+        _check("pace_linattn_backward", lib.pace_linattn_backward(
+            ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), g, cu, s0, d_o.data_ptr(), dst,
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ds0, None if ws is None else ws.data_ptr(), fl, s))
+    return dq, dk, dv, dS0
+
+
+def pace_linattn_step(S, q, k, v, log_decay, o=None, stream=None) -> torch.Tensor:
+    """One token for each of N sequences: q, k, v [N, H, d]; S fp32 [N, H, d, d] is updated in place; returns o."""
+    _need(isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3, "q: device tensor [N, H, d]")
+    _need(q.dtype in _IO_OF, f"q: bfloat16 or float32, not {q.dtype}")
+    n, H, d = q.shape
+    if o is None:
+        o = _new(q.shape, q.dtype, q, stream)
+    strides = []
+    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
+        rows, st = _rows(name, t, H, d, q)
+        _need(rows == n, f"{name}: {n} rows")
+        strides.append(st)
+    _need(S is not None, "S: the states")
+    sp = _plain("S", S, (n, H, d, d), torch.float32, q)
+    g = _plain("log_decay", log_decay, (H,), torch.float32, q)
+    desc = _LinattnDesc(n, H, d, d, _IO_OF[q.dtype], 0, 0, *strides)
+    with _On(q, stream) as s:
+        _check("pace_linattn_step", lib.pace_linattn_step(ctypes.byref(desc), sp, q.data_ptr(), k.data_ptr(),
+                                                          v.data_ptr(), g, o.data_ptr(), s))
+    return o
+
+
+_NORM_OF = {"l2": PACE_NORM_L2, "rms": PACE_NORM_RMS, PACE_NORM_L2: PACE_NORM_L2, PACE_NORM_RMS: PACE_NORM_RMS}
+
+
+def _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved, norm, eps, q_scale):
+    """Descriptor (strides of q and k set) and the addresses of weights, positions and frequencies."""
+    like = q if q is not None else k
+    _need(isinstance(like, torch.Tensor) and like.is_cuda and like.dim() >= 3, "q or k: device tensor [..., heads, d]")
+    _need(like.dtype in _IO_OF, f"q, k: bfloat16 or float32, not {like.dtype}")
+    _need(norm in _NORM_OF, "norm: 'l2' or 'rms'")
+    d = like.shape[-1]
+    heads, rows, strides = [0, 0], [], [0, 0]
+    for i, (name, t) in enumerate((("q", q), ("k", k))):
+        if t is None:
+            continue
+        _need(isinstance(t, torch.Tensor) and t.dim() >= 3, f"{name}: [..., heads, d]")
+        heads[i] = t.shape[-2]
+        n, strides[i] = _rows(name, t, heads[i], d, like)
+        rows.append(n)
+    _need(len(set(rows)) == 1, "q and k: as many rows")
+    half = int(rotary_dim) // 2
+    if rotary_dim:
+        _need(positions is not None and inv_freq is not None, "positions and inv_freq: given with rotary_dim")
+    _need(positions is None or positions.numel() == rows[0], f"positions: {rows[0]} of them")
+    ptrs = (_plain("q_weight", q_weight, (d,), torch.float32, like), _plain("k_weight", k_weight, (d,), torch.float32, like),
+            _plain("positions", positions, () if positions is None else positions.shape, torch.int32, like),
+            _plain("inv_freq", inv_freq, (half,), torch.float32, like))
+    desc = _QkNormDesc(rows[0], heads[0], heads[1], d, int(rotary_dim), int(bool(interleaved)), _NORM_OF[norm],
+                       _IO_OF[like.dtype], float(eps), float(q_scale), strides[0], strides[1], 0, 0)
+    return desc, like, heads, rows[0], d, ptrs
+
+
+def _opt(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, q_out=None, k_out=None,
+                        rotary_dim=0, interleaved=False, norm="rms", eps=1e-6, q_scale=1.0, stream=None):
+    """Queries and keys normalised for each head and turned by their position: returns (q_out, k_out).
+
+    q: [tokens, Hq, d], k: [tokens, Hk, d] (either may be None); q_out may be q, k_out may be k.
+    """
+    desc, like, heads, rows, d, ptrs = _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved,
+                                                norm, eps, q_scale)
+    outs = []
+    for i, (name, t, x) in enumerate((("q_out", q_out, q), ("k_out", k_out, k))):
+        _need(x is not None or t is None, f"{name}: given without its input")
+        if x is not None:
+            if t is None:
+                t = _new(x.shape, x.dtype, like, stream)
+            n, st = _rows(name, t, heads[i], d, like)
+            _need(n == rows, f"{name}: {rows} rows")
+            if i:
+                desc.k_out_stride = st
+            else:
+                desc.q_out_stride = st
+        outs.append(t)
+    with _On(like, stream) as s:
+        _check("pace_qk_norm_rotate", lib.pace_qk_norm_rotate(ctypes.byref(desc), _opt(q), _opt(k), *ptrs, _opt(outs[0]),
+                                                              _opt(outs[1]), s))
+    return tuple(outs)
+
+
+def pace_qk_norm_workspace_bytes(num_tokens: int, num_q_heads: int, num_k_heads: int, head_dim: int, io: int) -> int:
+    desc = _QkNormDesc(num_tokens, num_q_heads, num_k_heads, head_dim, 0, 0, PACE_NORM_RMS, io, 1e-6, 1.0, 0, 0, 0, 0)
+    n = ctypes.c_size_t()
+    _check("pace_qk_norm_workspace_bytes", lib.pace_qk_norm_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k_out, dq=None, dk=None,
+                                 dq_weight=None, dk_weight=None, rotary_dim=0, interleaved=False, norm="rms", eps=1e-6,
+                                 q_scale=1.0, workspace=None, stream=None):
+    """Gradients of pace_qk_norm_rotate: returns (dq, dk, dq_weight, dk_weight); a weight's gradient is made where the
+    weight is given (or a tensor for it)."""
+    desc, like, heads, rows, d, ptrs = _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved,
+                                                norm, eps, q_scale)
+    outs, grads, dws = [], [], []
+    for i, (x, dy, dx, w, dw) in enumerate(((q, d_q_out, dq, q_weight, dq_weight), (k, d_k_out, dk, k_weight, dk_weight))):
+        name = "qk"[i]
+        _need((x is None) == (dy is None), f"d_{name}_out: given with {name}")
+        if x is None:
+            _need(dx is None and dw is None, f"d{name}: given without {name}")
+            outs.append(None), grads.append(None), dws.append(None)
+            continue
+        n, st = _rows(f"d_{name}_out", dy, heads[i], d, like)
+        _need(n == rows and (n <= 1 or st in (0, heads[i] * d)), f"d_{name}_out: {rows} packed rows")
+        if dx is None:
+            dx = _new(x.shape, x.dtype, like, stream)
+        n, st = _rows(f"d{name}", dx, heads[i], d, like)
+        _need(n == rows, f"d{name}: {rows} rows")
+        if i:
+            desc.k_out_stride = st
+        else:
+            desc.q_out_stride = st
+        if dw is None and w is not None:
+            dw = _new((d,), torch.float32, like, stream)
+        outs.append(dx), grads.append(dy), dws.append(dw)
+    dwp = [_plain("dq_weight", dws[0], (d,), torch.float32, like), _plain("dk_weight", dws[1], (d,), torch.float32, like)]
+    ws = None
+    if dwp[0] is not None or dwp[1] is not None:
+        size = ctypes.c_size_t()
+        _check("pace_qk_norm_rotate_backward", lib.pace_qk_norm_workspace_bytes(ctypes.byref(desc), ctypes.byref(size)))
+        ws = _workspace("pace_qk_norm_rotate_backward", size.value, workspace, like, stream)
+    with _On(like, stream) as s:
+        _check("pace_qk_norm_rotate_backward", lib.pace_qk_norm_rotate_backward(
+            ctypes.byref(desc), _opt(q), _opt(k), *ptrs, _opt(grads[0]), _opt(grads[1]), _opt(outs[0]), _opt(outs[1]),
+            *dwp, _opt(ws), s))
+    return outs[0], outs[1], dws[0], dws[1]
 
 
 def pace_status_string(status: int) -> str:

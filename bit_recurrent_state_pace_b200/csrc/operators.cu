@@ -1,0 +1,228 @@
+// Host side of the linear-attention and query/key-norm entry points:
+// argument checks, workspace layout, launches.  Nothing here throws.
+#include <cmath>
+#include <string.h>
+
+#include "linattn.cuh"
+
+namespace {
+
+inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+inline pace_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return PACE_OK;
+  (void)cudaGetLastError();  // clear a non-sticky error so later calls start clean
+  return PACE_ERR_CUDA;
+}
+
+// Row stride in elements: 0 stands for packed rows of `width` elements; others hold a whole row and leave every
+// offset inside 63 bits.
+inline bool stride_ok(int64_t given, int64_t width, int64_t* out) {
+  *out = given == 0 ? width : given;
+  return *out >= width && *out <= ((int64_t)1 << 30);
+}
+
+struct LinShape {
+  int64_t qs, ks, vs, os;
+  size_t esz;
+};
+
+pace_status check_lin(const pace_linattn_desc* d, LinShape* s, bool tokens) {
+  if (!d) return PACE_ERR_INVALID_ARG;
+  if (d->num_seqs < 1 || d->num_heads < 1 || d->num_heads > PACE_MAX_HEADS) return PACE_ERR_INVALID_ARG;
+  if (d->d_k < 1 || d->d_v < 1) return PACE_ERR_INVALID_ARG;
+  if (d->io_dtype != PACE_IO_BF16 && d->io_dtype != PACE_IO_F32) return PACE_ERR_INVALID_ARG;
+  if (tokens && (d->total_tokens < 0 || d->max_len < 0)) return PACE_ERR_INVALID_ARG;
+  const int64_t w = (int64_t)d->num_heads * d->d_k;
+  if (d->d_k != d->d_v) return PACE_ERR_UNSUPPORTED;
+  if (d->d_k != 32 && d->d_k != 64 && d->d_k != 128) return PACE_ERR_UNSUPPORTED;
+  if (!stride_ok(d->q_stride, w, &s->qs) || !stride_ok(d->k_stride, w, &s->ks) || !stride_ok(d->v_stride, w, &s->vs) ||
+      !stride_ok(d->o_stride, w, &s->os))
+    return PACE_ERR_INVALID_ARG;
+  if (tokens && (d->total_tokens > 0x7fffffffll || d->max_len > 0x7fffffffll)) return PACE_ERR_UNSUPPORTED;
+  if ((int64_t)d->num_seqs * d->num_heads > (0x7fffffffll >> 4)) return PACE_ERR_UNSUPPORTED;   // grid sizes
+  s->esz = (size_t)pace::io_size(d->io_dtype);
+  return PACE_OK;
+}
+
+// io tensors and states; `need` says whether NULL is refused
+inline bool io_ok(const void* p, size_t esz, bool need) { return p ? aligned(p, esz) : !need; }
+inline bool state_ok(const float* p) { return aligned(p, 16); }
+
+pace::LinArgs lin_args(const pace_linattn_desc* d, const float* log_decay, const int32_t* cu, uint32_t* flags) {
+  pace::LinArgs a;
+  memset(&a, 0, sizeof a);
+  a.N = d->num_seqs;
+  a.H = d->num_heads;
+  a.D = d->d_k;
+  a.io = d->io_dtype;
+  a.total = (int32_t)d->total_tokens;
+  a.max_len = (int32_t)d->max_len;
+  a.cu = cu;
+  a.log_decay = log_decay;
+  a.flags = flags;
+  return a;
+}
+
+struct NormShape { int64_t qs, ks, qo, ko; size_t esz; };
+
+pace_status check_norm(const pace_qk_norm_desc* d, NormShape* s) {
+  if (!d) return PACE_ERR_INVALID_ARG;
+  if (d->num_tokens < 0 || d->num_q_heads < 0 || d->num_k_heads < 0 || d->num_q_heads > PACE_MAX_HEADS ||
+      d->num_k_heads > PACE_MAX_HEADS || d->num_q_heads + d->num_k_heads == 0)
+    return PACE_ERR_INVALID_ARG;
+  if (d->head_dim < 1 || d->rotary_dim < 0 || d->rotary_dim > d->head_dim || d->rotary_dim % 2) return PACE_ERR_INVALID_ARG;
+  if (d->interleaved != 0 && d->interleaved != 1) return PACE_ERR_INVALID_ARG;
+  if (d->norm != PACE_NORM_L2 && d->norm != PACE_NORM_RMS) return PACE_ERR_INVALID_ARG;
+  if (d->io_dtype != PACE_IO_BF16 && d->io_dtype != PACE_IO_F32) return PACE_ERR_INVALID_ARG;
+  if (!(d->eps > 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->q_scale)) return PACE_ERR_INVALID_ARG;
+  const int64_t wq = (int64_t)d->num_q_heads * d->head_dim, wk = (int64_t)d->num_k_heads * d->head_dim;
+  if (!stride_ok(d->q_stride, wq, &s->qs) || !stride_ok(d->k_stride, wk, &s->ks) ||
+      !stride_ok(d->q_out_stride, wq, &s->qo) || !stride_ok(d->k_out_stride, wk, &s->ko))
+    return PACE_ERR_INVALID_ARG;
+  if (d->head_dim % 8 || d->head_dim > 256 || d->num_tokens > 0x7fffffffll) return PACE_ERR_UNSUPPORTED;
+  s->esz = (size_t)pace::io_size(d->io_dtype);
+  return PACE_OK;
+}
+
+pace_status norm_args(const pace_qk_norm_desc* d, const NormShape& s, const void* q, const void* k, const float* wq,
+                      const float* wk, const int32_t* pos, const float* inv, void* qo, void* ko, pace::NormArgs* a) {
+  const bool any = d->num_tokens > 0;
+  if (!io_ok(q, s.esz, any && d->num_q_heads) || !io_ok(qo, s.esz, any && d->num_q_heads) ||
+      !io_ok(k, s.esz, any && d->num_k_heads) || !io_ok(ko, s.esz, any && d->num_k_heads))
+    return PACE_ERR_INVALID_ARG;
+  if (d->rotary_dim && (!inv || (any && !pos))) return PACE_ERR_INVALID_ARG;
+  if (!aligned(wq, 4) || !aligned(wk, 4) || !aligned(pos, 4) || !aligned(inv, 4)) return PACE_ERR_INVALID_ARG;
+  memset(a, 0, sizeof *a);
+  a->tokens = (int32_t)d->num_tokens;
+  a->D = d->head_dim;
+  a->rot = d->rotary_dim;
+  a->interleaved = d->interleaved;
+  a->io = d->io_dtype;
+  a->inv_n = d->norm == PACE_NORM_RMS ? 1.f / (float)d->head_dim : 1.f;
+  a->eps = d->eps;
+  a->pos = pos;
+  a->inv_freq = inv;
+  a->side[0] = pace::NormSide{q, nullptr, qo, wq, nullptr, s.qs, s.qo, d->num_q_heads, d->q_scale};
+  a->side[1] = pace::NormSide{k, nullptr, ko, wk, nullptr, s.ks, s.ko, d->num_k_heads, 1.f};
+  return PACE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pace_status pace_linattn_workspace_bytes(const pace_linattn_desc* desc, int32_t backward, size_t* bytes) {
+  LinShape s;
+  if (!bytes || (backward != 0 && backward != 1)) return PACE_ERR_INVALID_ARG;
+  const pace_status st = check_lin(desc, &s, true);
+  if (st != PACE_OK) return st;
+  *bytes = 0;
+  return PACE_OK;
+}
+
+pace_status pace_linattn_forward(const pace_linattn_desc* desc, const void* q, const void* k, const void* v,
+                                 const float* log_decay, const int32_t* cu_seqlens, const float* S0, void* o,
+                                 float* ST, void* d_workspace, uint32_t* d_flags, void* stream) {
+  LinShape s;
+  const pace_status st = check_lin(desc, &s, true);
+  if (st != PACE_OK) return st;
+  if (!cu_seqlens && desc->total_tokens != (int64_t)desc->num_seqs * desc->max_len) return PACE_ERR_INVALID_ARG;
+  const bool any = desc->total_tokens > 0;
+  if (!io_ok(q, s.esz, any) || !io_ok(k, s.esz, any) || !io_ok(v, s.esz, any) || !io_ok(o, s.esz, any))
+    return PACE_ERR_INVALID_ARG;
+  if (!log_decay || !aligned(log_decay, 4) || !aligned(cu_seqlens, 4) || !state_ok(S0) || !state_ok(ST) ||
+      !aligned(d_flags, 4) || !aligned(d_workspace, 256))
+    return PACE_ERR_INVALID_ARG;
+  pace::LinArgs a = lin_args(desc, log_decay, cu_seqlens, d_flags);
+  a.walks = 1;
+  a.walk[0] = pace::LinWalk{q, k, v, o, s.qs, s.ks, s.vs, s.os, S0, ST, 0, 0};
+  return from_cuda(pace::launch_linattn_stream(a, as_stream(stream)));
+}
+
+pace_status pace_linattn_backward(const pace_linattn_desc* desc, const void* q, const void* k, const void* v,
+                                  const float* log_decay, const int32_t* cu_seqlens, const float* S0,
+                                  const void* d_o, const float* dST, void* dq, void* dk, void* dv, float* dS0,
+                                  void* d_workspace, uint32_t* d_flags, void* stream) {
+  LinShape s;
+  const pace_status st = check_lin(desc, &s, true);
+  if (st != PACE_OK) return st;
+  if (!cu_seqlens && desc->total_tokens != (int64_t)desc->num_seqs * desc->max_len) return PACE_ERR_INVALID_ARG;
+  const bool any = desc->total_tokens > 0;
+  if (!io_ok(q, s.esz, any) || !io_ok(k, s.esz, any) || !io_ok(v, s.esz, any) || !io_ok(d_o, s.esz, any) ||
+      !io_ok(dq, s.esz, any) || !io_ok(dk, s.esz, any) || !io_ok(dv, s.esz, any))
+    return PACE_ERR_INVALID_ARG;
+  if (!log_decay || !aligned(log_decay, 4) || !aligned(cu_seqlens, 4) || !state_ok(S0) || !state_ok(dST) ||
+      !state_ok(dS0) || !aligned(d_flags, 4) || !aligned(d_workspace, 256))
+    return PACE_ERR_INVALID_ARG;
+  if (dS0 && (dS0 == dST || dS0 == S0)) return PACE_ERR_INVALID_ARG;
+  pace::LinArgs a = lin_args(desc, log_decay, cu_seqlens, d_flags);
+  a.walks = 3;
+  a.walk[0] = pace::LinWalk{k, q, d_o, dv, s.ks, s.qs, s.os, s.vs, dST, dS0, 1, 0};
+  a.walk[1] = pace::LinWalk{v, d_o, q, dk, s.vs, s.os, s.qs, s.ks, dST, nullptr, 1, 1};
+  a.walk[2] = pace::LinWalk{d_o, v, k, dq, s.os, s.vs, s.ks, s.qs, S0, nullptr, 0, 1};
+  return from_cuda(pace::launch_linattn_stream(a, as_stream(stream)));
+}
+
+pace_status pace_linattn_step(const pace_linattn_desc* desc, float* S, const void* q, const void* k, const void* v,
+                              const float* log_decay, void* o, void* stream) {
+  LinShape s;
+  const pace_status st = check_lin(desc, &s, false);
+  if (st != PACE_OK) return st;
+  if (!S || !state_ok(S) || !log_decay || !aligned(log_decay, 4) || !io_ok(q, s.esz, true) || !io_ok(k, s.esz, true) ||
+      !io_ok(v, s.esz, true) || !io_ok(o, s.esz, true))
+    return PACE_ERR_INVALID_ARG;
+  return from_cuda(pace::launch_linattn_step(S, q, k, v, log_decay, o, s.qs, s.ks, s.vs, s.os, desc->num_seqs,
+                                             desc->num_heads, desc->d_k, desc->io_dtype, as_stream(stream)));
+}
+
+pace_status pace_qk_norm_rotate(const pace_qk_norm_desc* desc, const void* q, const void* k, const float* q_weight,
+                                const float* k_weight, const int32_t* positions, const float* inv_freq, void* q_out,
+                                void* k_out, void* stream) {
+  NormShape s;
+  pace::NormArgs a;
+  pace_status st = check_norm(desc, &s);
+  if (st == PACE_OK) st = norm_args(desc, s, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, &a);
+  if (st != PACE_OK) return st;
+  if ((q && q_out == q && s.qs != s.qo) || (k && k_out == k && s.ks != s.ko)) return PACE_ERR_INVALID_ARG;
+  return from_cuda(pace::launch_qk_norm(a, as_stream(stream)));
+}
+
+pace_status pace_qk_norm_workspace_bytes(const pace_qk_norm_desc* desc, size_t* bytes) {
+  NormShape s;
+  if (!bytes) return PACE_ERR_INVALID_ARG;
+  const pace_status st = check_norm(desc, &s);
+  if (st != PACE_OK) return st;
+  *bytes = pace::qk_norm_partial_bytes(desc->num_tokens, desc->head_dim);
+  return PACE_OK;
+}
+
+pace_status pace_qk_norm_rotate_backward(const pace_qk_norm_desc* desc, const void* q, const void* k,
+                                         const float* q_weight, const float* k_weight, const int32_t* positions,
+                                         const float* inv_freq, const void* d_q_out, const void* d_k_out, void* dq,
+                                         void* dk, float* dq_weight, float* dk_weight, void* d_workspace,
+                                         void* stream) {
+  NormShape s;
+  pace::NormArgs a;
+  pace_status st = check_norm(desc, &s);
+  if (st == PACE_OK) st = norm_args(desc, s, q, k, q_weight, k_weight, positions, inv_freq, dq, dk, &a);
+  if (st != PACE_OK) return st;
+  const bool any = desc->num_tokens > 0;
+  if (!io_ok(d_q_out, s.esz, any && desc->num_q_heads) || !io_ok(d_k_out, s.esz, any && desc->num_k_heads))
+    return PACE_ERR_INVALID_ARG;
+  const int64_t wq = (int64_t)desc->num_q_heads * desc->head_dim, wk = (int64_t)desc->num_k_heads * desc->head_dim;
+  if ((d_q_out && dq == d_q_out && s.qo != wq) || (d_k_out && dk == d_k_out && s.ko != wk)) return PACE_ERR_INVALID_ARG;
+  if ((q && dq == q && s.qo != s.qs) || (k && dk == k && s.ko != s.ks)) return PACE_ERR_INVALID_ARG;
+  if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return PACE_ERR_INVALID_ARG;
+  if ((dq_weight || dk_weight) && (!d_workspace || !aligned(d_workspace, 256))) return PACE_ERR_INVALID_ARG;
+  a.side[0].dy = d_q_out;
+  a.side[1].dy = d_k_out;
+  a.side[0].dw = dq_weight;
+  a.side[1].dw = dk_weight;
+  a.partial = reinterpret_cast<float*>(d_workspace);
+  return from_cuda(pace::launch_qk_norm_backward(a, as_stream(stream)));
+}
+
+}  // extern "C"

@@ -434,6 +434,147 @@ pace_status pace_decay_rates(const void* alpha, int64_t rows, int32_t num_heads,
 pace_status pace_select_head_bits(const double* rates, int32_t num_heads, int32_t num_int8,
                                   uint8_t* head_bits);
 
+/*
+ * Linear attention with one fixed decay for each head (retention): the plain
+ * write rule, without the delta rule's erasure, that layers of a hybrid stack
+ * use beside a gated-delta layer.  For head h with log decay g_h:
+ *   S_t = exp(g_h) S_{t-1} + v_t k_t^T,   o_t = S_t q_t,
+ * S in R^{d_v x d_k} as above, fp32.  No 1/sqrt(d) is applied: scale q (as
+ * pace_qk_norm_rotate does).  The pages give no such operator.
+ *
+ * Layout: prompts lie packed one behind the other.  Row r of q, k, v, o and
+ * of their gradients is token r of all sequences together, [num_heads][d]
+ * elements of io_dtype, and begins `stride` elements behind row r - 1 (0:
+ * num_heads * d), so the tensors may be parts of a wider projection.
+ * cu_seqlens (device int32 [num_seqs + 1], ascending): sequence n is rows
+ * [cu_seqlens[n], cu_seqlens[n + 1]); NULL: every sequence has max_len rows
+ * and total_tokens = num_seqs * max_len.  Offsets outside [0, total_tokens]
+ * are moved to its edge, a sequence that would end before it begins is
+ * empty.  Rows of no sequence are neither read nor written; the state behind
+ * an empty sequence is the state before it.  max_len only guides how the
+ * work is split when cu_seqlens is given: results hold for longer sequences.
+ *
+ * log_decay: device fp32 [num_heads], constants of the layer (no gradient);
+ * <= 0, -inf: no memory.
+ * States: device fp32 [num_seqs][num_heads][d_v][d_k], 16-byte aligned.
+ * io tensors are aligned to the element size.  Outputs do not overlap inputs
+ * or one another except where said.
+ * A NaN or Inf reaches the outputs that the formulas give it to; in bf16 it
+ * may also reach outputs of up to 63 tokens of the same sequence and head
+ * before it (behind it, in the gradients for k and v).
+ */
+typedef struct {
+  int32_t num_seqs;          /* N >= 1 */
+  int32_t num_heads;         /* H: 1..256 */
+  int32_t d_k, d_v;          /* head dims; supported: d_k == d_v in {32, 64, 128} */
+  int32_t io_dtype;          /* pace_io_dtype */
+  int64_t total_tokens;      /* rows of q, k, v, o: 0 .. 2^31 - 1 */
+  int64_t max_len;           /* longest sequence (see cu_seqlens) */
+  int64_t q_stride, k_stride, v_stride, o_stride;   /* elements from row to row; 0 = num_heads * d.
+                                the gradients dq, dk, dv and d_o have the strides of q, k, v, o */
+} pace_linattn_desc;
+
+/* Bytes of device workspace that pace_linattn_forward (backward = 0) or
+ * pace_linattn_backward (backward = 1) needs for this descriptor (may be 0).
+ * Host-only, no CUDA call. */
+pace_status pace_linattn_workspace_bytes(const pace_linattn_desc* desc, int32_t backward, size_t* bytes);
+
+/*
+ * Prompts in chunked form.  S0: states before the first tokens, or NULL for
+ * zeros.  o: every token's output (io_dtype).  ST: receives the states
+ * behind the last tokens, or NULL; ST may be S0.
+ * d_workspace: pace_linattn_workspace_bytes bytes, 256-byte aligned, not
+ * used by anything else until the work on `stream` is done (two graphs that
+ * may run side by side need one each); NULL where 0 bytes are needed.
+ * d_flags: optional device uint32; receives PACE_FLAG_TIMEOUT by atomic OR
+ * if a bounded wait inside a kernel gave up.  Enqueues only, allocates
+ * nothing; may be captured into a graph.
+ */
+pace_status pace_linattn_forward(const pace_linattn_desc* desc, const void* q, const void* k, const void* v,
+                                 const float* log_decay, const int32_t* cu_seqlens, const float* S0, void* o,
+                                 float* ST, void* d_workspace, uint32_t* d_flags, void* stream);
+
+/*
+ * Gradients of pace_linattn_forward, recomputed from its inputs.  With X_T =
+ * dST (the gradient that reaches ST; NULL: zero) and, from the last token
+ * back, D_t = X_t + do_t q_t^T:
+ *   dq_t = S_t^T do_t,  dk_t = D_t^T v_t,  dv_t = D_t k_t,
+ *   X_{t-1} = exp(g_h) D_t,   dS0 = X_0  (dS0 NULL: not wanted).
+ * dq, dk, dv: io_dtype, in the strides of q, k, v; d_o in that of o.  dS0
+ * does not overlap dST or S0.  Bit for bit the same on every call.
+ */
+pace_status pace_linattn_backward(const pace_linattn_desc* desc, const void* q, const void* k, const void* v,
+                                  const float* log_decay, const int32_t* cu_seqlens, const float* S0,
+                                  const void* d_o, const float* dST, void* dq, void* dk, void* dv, float* dS0,
+                                  void* d_workspace, uint32_t* d_flags, void* stream);
+
+/*
+ * One token for every sequence in recurrent form: row n of q, k, v, o is
+ * sequence n's token (total_tokens and max_len are not looked at, the
+ * strides are), S its states, updated in place.  Enqueues only.
+ */
+pace_status pace_linattn_step(const pace_linattn_desc* desc, float* S, const void* q, const void* k, const void* v,
+                              const float* log_decay, void* o, void* stream);
+
+/*
+ * Queries and keys, normalised for each head and turned by their position in
+ * one pass: what pace_decode_step, pace_prefill and the linear attention
+ * above take as q and k.  For a row x of one head (d elements):
+ *   y = s R(pos) (w * x r),   r = (sum_i x_i^2 / n + eps)^(-1/2),
+ * n = d (PACE_NORM_RMS) or 1 (PACE_NORM_L2), w the weights (NULL: ones), s =
+ * q_scale for queries and 1 for keys.  R(pos) turns rotary_dim / 2 pairs of
+ * channels, pair i by the angle pos * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * pair i being channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where
+ * `interleaved` is 1; channels from rotary_dim on are not turned.  The angle
+ * is reduced in fp64, so far positions turn as exactly as near ones.  The
+ * pages only say that q and k come normalised.
+ *
+ * q: [num_tokens] rows of [num_q_heads][d], k: of [num_k_heads][d], strides
+ * as in pace_linattn_desc; q_weight, k_weight: device fp32 [d] or NULL;
+ * positions: device int32 [num_tokens], inv_freq: device fp32
+ * [rotary_dim / 2] (both NULL where rotary_dim is 0).  q_out may be q and
+ * k_out may be k (with equal strides).  Sums of squares are fp32: rows whose
+ * sum overflows give zeros, as the formula in fp32 does.
+ */
+typedef enum { PACE_NORM_L2 = 0, PACE_NORM_RMS = 1 } pace_norm_kind;
+
+typedef struct {
+  int64_t num_tokens;                    /* 0 .. 2^31 - 1 */
+  int32_t num_q_heads, num_k_heads;      /* 0..256 each; q (k) and its outputs NULL where 0 */
+  int32_t head_dim;                      /* d: a multiple of 8, 8..256 */
+  int32_t rotary_dim;                    /* even, 0..d */
+  int32_t interleaved;                   /* 0 or 1 */
+  int32_t norm;                          /* pace_norm_kind */
+  int32_t io_dtype;                      /* pace_io_dtype */
+  float eps;                             /* > 0 */
+  float q_scale;                         /* finite */
+  int64_t q_stride, k_stride;            /* elements from token to token; 0 = heads * d */
+  int64_t q_out_stride, k_out_stride;    /* of q_out, k_out, or of dq, dk */
+} pace_qk_norm_desc;
+
+pace_status pace_qk_norm_rotate(const pace_qk_norm_desc* desc, const void* q, const void* k, const float* q_weight,
+                                const float* k_weight, const int32_t* positions, const float* inv_freq, void* q_out,
+                                void* k_out, void* stream);
+
+/*
+ * Its gradients.  d_q_out, d_k_out: the gradients of the outputs, rows packed
+ * ([num_tokens][heads][d]); dq, dk: with the out strides, may be d_q_out and
+ * d_k_out where those are packed.  With u = s R(-pos) dy, x^ = x r:
+ *   dw = sum over tokens and heads of u * x^,  h = u * w,
+ *   dx = r (h - x^ (x^ . h) / n).
+ * dq_weight, dk_weight: device fp32 [d], overwritten, or NULL.
+ * d_workspace: pace_qk_norm_workspace_bytes bytes, 256-byte aligned, as in
+ * pace_linattn_forward; NULL where no weight gradient is wanted.  Sums run in
+ * a fixed order: bit for bit the same on every call.
+ */
+pace_status pace_qk_norm_workspace_bytes(const pace_qk_norm_desc* desc, size_t* bytes);
+pace_status pace_qk_norm_rotate_backward(const pace_qk_norm_desc* desc, const void* q, const void* k,
+                                         const float* q_weight, const float* k_weight, const int32_t* positions,
+                                         const float* inv_freq, const void* d_q_out, const void* d_k_out, void* dq,
+                                         void* dk, float* dq_weight, float* dk_weight, void* d_workspace,
+                                         void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* pace_status_string(pace_status s);
 
