@@ -12,20 +12,95 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 
 // ---- the walk ------------------------------------------------------------------
-// A block walks one sequence and head for 32 rows of S.  Four threads share a
-// row; a thread holds the columns 4 (c + 4 e) .. + 3 of it in registers, so that
-// the four threads' reads of a key or query are 64 contiguous bytes.  The state
-// never leaves the registers; tokens come through shared memory, TT at a time,
-// the next ones being loaded while these are used.
+// A block walks one sequence and head for 32 rows of S, which never leave the
+// registers: sixteen threads hold four rows, D / 16 columns of them each, so
+// that a token costs a thread 8 D / 32 packed products for a few loads of its
+// key, query and value from shared memory.  Tokens come there TT at a time,
+// the next ones being loaded while these are used; the outputs of four tokens
+// and four rows are summed over the sixteen threads together.
+//
+// Within TT tokens S is kept without its decay: token t adds value / A^p key^T
+// (p tokens of decay so far) and reads A^p S query, and the decay of all TT is
+// applied once, in 48 bits -- a product each token would cost half as much
+// again and, by a fixed rounding of A, several 1e-6 of a state that remembers
+// hundreds of tokens.  Heads that forget faster than A^-TT can hold (g < -3)
+// take the product each token.
 constexpr int kWalkThreads = 128, kRows = 32, TT = 16;
+
+template <int D>
+struct WalkSmem {
+  float q[TT][D], k[TT][D];
+  float v[TT][kRows], o[TT][kRows];
+  float up[TT + 1], down[TT + 1], down_lo[TT + 1];   // A^-p, A^p and the rest of A^p
+};
+
+template <int D, bool BACK, bool FAST>
+__device__ __forceinline__ void walk_tokens(WalkSmem<D>& sm, float2 (&S)[4][D / 32], int m, int rg, int c, float al) {
+  constexpr int CP = D / 32;                         // column pairs of a thread
+  constexpr int W = CP < 2 ? 1 : 2;                  // pairs a load
+  const float2 a2 = make_float2(al, al);
+  for (int t0 = 0; t0 < m; t0 += 4) {
+    float acc[4][4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + u;                          // tokens from m on hold zeros
+      const float4 v4 = *reinterpret_cast<const float4*>(&sm.v[t][4 * rg]);
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+      float2 k2[CP], q2[CP];
+#pragma unroll
+      for (int e = 0; e < CP; e += W) {
+        const int col = 2 * W * c + 32 * e;
+        if (W == 2) {
+          const float4 kk = *reinterpret_cast<const float4*>(&sm.k[t][col]);
+          const float4 qq = *reinterpret_cast<const float4*>(&sm.q[t][col]);
+          k2[e] = make_float2(kk.x, kk.y), k2[e + W - 1] = make_float2(kk.z, kk.w);
+          q2[e] = make_float2(qq.x, qq.y), q2[e + W - 1] = make_float2(qq.z, qq.w);
+        } else {
+          k2[e] = *reinterpret_cast<const float2*>(&sm.k[t][col]);
+          q2[e] = *reinterpret_cast<const float2*>(&sm.q[t][col]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float2 v2 = make_float2(v[r], v[r]);
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < CP; ++e) {
+          float2 x = S[r][e];
+          if (FAST && !BACK && t < m) x = __fmul2_rn(x, a2);
+          x = __ffma2_rn(v2, k2[e], x);
+          s = __ffma2_rn(x, q2[e], s);
+          if (FAST && BACK && t < m) x = __fmul2_rn(x, a2);
+          S[r][e] = x;
+        }
+        acc[u][r] = s.x + s.y;
+      }
+    }
+    // sums over the 16 threads: each step halves the values a thread keeps; thread c ends with token c / 4, row c % 4
+    float h8[8], h4[4], h2[2];
+    const bool b3 = c & 8, b2 = c & 4, b1 = c & 2, b0 = c & 1;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float lo = acc[x >> 2][x & 3], hi = acc[2 + (x >> 2)][x & 3];
+      h8[x] = (b3 ? hi : lo) + __shfl_xor_sync(FULL, b3 ? lo : hi, 8);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) h4[x] = (b2 ? h8[4 + x] : h8[x]) + __shfl_xor_sync(FULL, b2 ? h8[x] : h8[4 + x], 4);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) h2[x] = (b1 ? h4[2 + x] : h4[x]) + __shfl_xor_sync(FULL, b1 ? h4[x] : h4[2 + x], 2);
+    const float o = (b0 ? h2[1] : h2[0]) + __shfl_xor_sync(FULL, b0 ? h2[0] : h2[1], 1);
+    const int t = t0 + (c >> 2);
+    sm.o[t][4 * rg + (c & 3)] = FAST ? o : o * sm.down[BACK ? t : t + 1];
+  }
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const __grid_constant__ LinArgs a) {
-  constexpr int V4 = D / 16;                         // float4 groups of a thread
+  constexpr int CP = D / 32, W = CP < 2 ? 1 : 2;
   constexpr int QKN = TT * D / kWalkThreads, VN = TT * kRows / kWalkThreads;
-  __shared__ __align__(16) float qs[TT][D], ks[TT][D];
-  __shared__ float vs[TT][kRows], os[TT][kRows];
-  const int tid = threadIdx.x, row = tid >> 2, c = tid & 3;
+  constexpr int IO = BF16 ? PACE_IO_BF16 : PACE_IO_F32;
+  __shared__ __align__(16) WalkSmem<D> sm;
+  const int tid = threadIdx.x, rg = tid >> 4, c = tid & 15;
   constexpr int SL = D / kRows;                      // row slices of a state
   const int slice = blockIdx.x % SL;
   const int rest = blockIdx.x / SL;
@@ -34,22 +109,28 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const __grid
   int begin, end;
   seq_rows(a, n, &begin, &end);
   const int len = end - begin;
-  const float al = expf(clamp_log_decay(a.log_decay[h]));
+  const float g = clamp_log_decay(a.log_decay[h]), al = expf(g);
+  const bool fast = !(g >= -3.f);
+  if (tid <= TT) {
+    const double d = exp((double)g * tid);
+    sm.down[tid] = (float)d;
+    sm.down_lo[tid] = (float)(d - (double)(float)d);
+    sm.up[tid] = fast ? 1.f : (float)exp(-(double)g * tid);
+  }
   const size_t st0 = ((size_t)n * a.H + h) * D * D;
-  const int i = slice * kRows + row;                 // this thread's row of S
-  float2 S[V4 * 2];
+  float2 S[4][CP];
 #pragma unroll
-  for (int e = 0; e < V4; ++e) {
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (w.S_in) {
+  for (int r = 0; r < 4; ++r) {
+    const int i = slice * kRows + 4 * rg + r;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = 4 * (c + 4 * e) + j;
-        x[j] = w.S_in[st0 + (w.swap ? (size_t)col * D + i : (size_t)i * D + col)];
+    for (int e = 0; e < CP; ++e) {
+      const int col = 2 * W * c + 32 * (e / W) * W + 2 * (e % W);
+      S[r][e] = make_float2(0.f, 0.f);
+      if (w.S_in) {
+        S[r][e].x = w.S_in[st0 + (w.swap ? (size_t)col * D + i : (size_t)i * D + col)];
+        S[r][e].y = w.S_in[st0 + (w.swap ? (size_t)(col + 1) * D + i : (size_t)i * D + col + 1)];
       }
     }
-    S[2 * e] = make_float2(x[0], x[1]);
-    S[2 * e + 1] = make_float2(x[2], x[3]);
   }
   const size_t hd = (size_t)h * D;
   float nq[QKN], nk[QKN], nv[VN];
@@ -59,57 +140,44 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const __grid
       const int x = tid + e * kWalkThreads, t = t0 + x / D, j = x % D;
       const bool in = t < len;
       const size_t r = (size_t)(w.back ? end - 1 - t : begin + t);
-      nq[e] = in ? load_io(w.query, r * w.query_stride + hd + j, BF16 ? PACE_IO_BF16 : PACE_IO_F32) : 0.f;
-      nk[e] = in ? load_io(w.key, r * w.key_stride + hd + j, BF16 ? PACE_IO_BF16 : PACE_IO_F32) : 0.f;
+      nq[e] = in ? load_io(w.query, r * w.query_stride + hd + j, IO) : 0.f;
+      nk[e] = in ? load_io(w.key, r * w.key_stride + hd + j, IO) : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < VN; ++e) {
       const int x = tid + e * kWalkThreads, t = t0 + x / kRows, j = x % kRows;
       const size_t r = (size_t)(w.back ? end - 1 - t : begin + t);
-      nv[e] = t < len ? load_io(w.value, r * w.value_stride + hd + slice * kRows + j, BF16 ? PACE_IO_BF16 : PACE_IO_F32) : 0.f;
+      nv[e] = t < len ? load_io(w.value, r * w.value_stride + hd + slice * kRows + j, IO) : 0.f;
     }
   };
   fetch(0);
+  __syncthreads();                                   // the tables
   for (int t0 = 0; t0 < len; t0 += TT) {
 #pragma unroll
     for (int e = 0; e < QKN; ++e) {
       const int x = tid + e * kWalkThreads;
-      (&qs[0][0])[x] = nq[e];
-      (&ks[0][0])[x] = nk[e];
+      (&sm.q[0][0])[x] = nq[e];
+      (&sm.k[0][0])[x] = nk[e];
     }
 #pragma unroll
-    for (int e = 0; e < VN; ++e) (&vs[0][0])[tid + e * kWalkThreads] = nv[e];
+    for (int e = 0; e < VN; ++e) {
+      const int x = tid + e * kWalkThreads, t = x / kRows;
+      (&sm.v[0][0])[x] = nv[e] * sm.up[w.back ? t : t + 1];
+    }
     __syncthreads();
     if (t0 + TT < len) fetch(t0 + TT);
     const int m = min(TT, len - t0);
-    for (int t = 0; t < m; ++t) {
-      const float v = vs[t][row];
-      const float2 v2 = make_float2(v, v), a2 = make_float2(al, al);
-      float2 acc = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+    if (fast) {
+      if (w.back) walk_tokens<D, true, true>(sm, S, m, rg, c, al);
+      else walk_tokens<D, false, true>(sm, S, m, rg, c, al);
+    } else {
+      if (w.back) walk_tokens<D, true, false>(sm, S, m, rg, c, al);
+      else walk_tokens<D, false, false>(sm, S, m, rg, c, al);
+      const float2 hi = make_float2(sm.down[m], sm.down[m]), lo = make_float2(sm.down_lo[m], sm.down_lo[m]);
 #pragma unroll
-      for (int e = 0; e < V4; ++e) {
-        const float4 kk = *reinterpret_cast<const float4*>(&ks[t][4 * (c + 4 * e)]);
-        const float4 qq = *reinterpret_cast<const float4*>(&qs[t][4 * (c + 4 * e)]);
-        float2 x0 = S[2 * e], x1 = S[2 * e + 1];
-        if (!w.back) {
-          x0 = __fmul2_rn(x0, a2);
-          x1 = __fmul2_rn(x1, a2);
-        }
-        x0 = __ffma2_rn(v2, make_float2(kk.x, kk.y), x0);
-        x1 = __ffma2_rn(v2, make_float2(kk.z, kk.w), x1);
-        acc = __ffma2_rn(x0, make_float2(qq.x, qq.y), acc);
-        acc1 = __ffma2_rn(x1, make_float2(qq.z, qq.w), acc1);
-        if (w.back) {
-          x0 = __fmul2_rn(x0, a2);
-          x1 = __fmul2_rn(x1, a2);
-        }
-        S[2 * e] = x0;
-        S[2 * e + 1] = x1;
-      }
-      float s = (acc.x + acc.y) + (acc1.x + acc1.y);
-      s += __shfl_xor_sync(FULL, s, 1);
-      s += __shfl_xor_sync(FULL, s, 2);
-      if (c == 0) os[t][row] = s;
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < CP; ++e) S[r][e] = __ffma2_rn(S[r][e], hi, __fmul2_rn(S[r][e], lo));
     }
     __syncthreads();
 #pragma unroll
@@ -118,20 +186,20 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const __grid
       if (t < m) {
         const size_t r = (size_t)(w.back ? end - 1 - (t0 + t) : begin + t0 + t);
         const size_t at = r * w.out_stride + hd + slice * kRows + j;
-        if (BF16) reinterpret_cast<uint16_t*>(w.out)[at] = float_to_bf16_bits_rn(os[t][j]);
-        else reinterpret_cast<float*>(w.out)[at] = os[t][j];
+        if (BF16) reinterpret_cast<uint16_t*>(w.out)[at] = float_to_bf16_bits_rn(sm.o[t][j]);
+        else reinterpret_cast<float*>(w.out)[at] = sm.o[t][j];
       }
     }
-    __syncthreads();
   }
   if (w.S_out) {
 #pragma unroll
-    for (int e = 0; e < V4; ++e) {
-      const float x[4] = {S[2 * e].x, S[2 * e].y, S[2 * e + 1].x, S[2 * e + 1].y};
+    for (int r = 0; r < 4; ++r) {
+      const int i = slice * kRows + 4 * rg + r;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = 4 * (c + 4 * e) + j;
-        w.S_out[st0 + (w.swap ? (size_t)col * D + i : (size_t)i * D + col)] = x[j];
+      for (int e = 0; e < CP; ++e) {
+        const int col = 2 * W * c + 32 * (e / W) * W + 2 * (e % W);
+        w.S_out[st0 + (w.swap ? (size_t)col * D + i : (size_t)i * D + col)] = S[r][e].x;
+        w.S_out[st0 + (w.swap ? (size_t)(col + 1) * D + i : (size_t)i * D + col + 1)] = S[r][e].y;
       }
     }
   }

@@ -3,7 +3,7 @@
 #include <cmath>
 #include <string.h>
 
-#include "linattn.cuh"
+#include "linattn_tc.cuh"
 
 namespace {
 
@@ -66,6 +66,22 @@ pace::LinArgs lin_args(const pace_linattn_desc* d, const float* log_decay, const
   return a;
 }
 
+// Walks over all sequences, on the tensor cores where their shapes allow.
+inline pace::LinSplit split_of(const pace_linattn_desc* d, int walks) {
+  return pace::linattn_tc_split((int64_t)d->num_seqs * d->num_heads, d->max_len, walks);
+}
+inline size_t stretch_bytes(const pace_linattn_desc* d, int walks) {
+  const pace::LinSplit sp = split_of(d, walks);
+  if (sp.stretches <= 1) return 0;
+  return (size_t)walks * d->num_seqs * d->num_heads * sp.stretches * d->d_k * d->d_k * sizeof(float);
+}
+pace_status run_walks(const pace_linattn_desc* d, const pace::LinArgs& a, void* ws, cudaStream_t st) {
+  if (!pace::linattn_tc_takes(a)) return from_cuda(pace::launch_linattn_stream(a, st));
+  const pace::LinSplit sp = split_of(d, a.walks);
+  if (sp.stretches > 1 && !ws) return PACE_ERR_INVALID_ARG;
+  return from_cuda(pace::launch_linattn_tc(a, sp, reinterpret_cast<float*>(ws), st));
+}
+
 struct NormShape { int64_t qs, ks, qo, ko; size_t esz; };
 
 pace_status check_norm(const pace_qk_norm_desc* d, NormShape* s) {
@@ -120,6 +136,7 @@ pace_status pace_linattn_workspace_bytes(const pace_linattn_desc* desc, int32_t 
   const pace_status st = check_lin(desc, &s, true);
   if (st != PACE_OK) return st;
   *bytes = 0;
+  if (desc->io_dtype == PACE_IO_BF16 && desc->d_k >= 64) *bytes = stretch_bytes(desc, backward ? 3 : 1);
   return PACE_OK;
 }
 
@@ -139,7 +156,7 @@ pace_status pace_linattn_forward(const pace_linattn_desc* desc, const void* q, c
   pace::LinArgs a = lin_args(desc, log_decay, cu_seqlens, d_flags);
   a.walks = 1;
   a.walk[0] = pace::LinWalk{q, k, v, o, s.qs, s.ks, s.vs, s.os, S0, ST, 0, 0};
-  return from_cuda(pace::launch_linattn_stream(a, as_stream(stream)));
+  return run_walks(desc, a, d_workspace, as_stream(stream));
 }
 
 pace_status pace_linattn_backward(const pace_linattn_desc* desc, const void* q, const void* k, const void* v,
@@ -163,7 +180,7 @@ pace_status pace_linattn_backward(const pace_linattn_desc* desc, const void* q, 
   a.walk[0] = pace::LinWalk{k, q, d_o, dv, s.ks, s.qs, s.os, s.vs, dST, dS0, 1, 0};
   a.walk[1] = pace::LinWalk{v, d_o, q, dk, s.vs, s.os, s.qs, s.ks, dST, nullptr, 1, 1};
   a.walk[2] = pace::LinWalk{d_o, v, k, dq, s.os, s.vs, s.ks, s.qs, S0, nullptr, 0, 1};
-  return from_cuda(pace::launch_linattn_stream(a, as_stream(stream)));
+  return run_walks(desc, a, d_workspace, as_stream(stream));
 }
 
 pace_status pace_linattn_step(const pace_linattn_desc* desc, float* S, const void* q, const void* k, const void* v,
