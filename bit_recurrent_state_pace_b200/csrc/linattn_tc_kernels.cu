@@ -45,13 +45,13 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int C = 64;                 // tokens a chunk
 constexpr int NST = 3;                // staged chunks
-constexpr int kTcThreads = 512;
+constexpr int kTcThreads = 896;
 constexpr int kSms = 148;             // B200
 
-// TMEM columns
-constexpr uint32_t T_SC = 0, T_OI = 64, T_OP = 128, T_U = 192, T_S = 320, T_VR = 384, T_V = 416;
+// TMEM columns.  All 512 are allocated, so the allocation begins at column 0.
+constexpr uint32_t T_SC = 0, T_OI = 64, T_OP = 128, T_U = 192, T_S = 320, T_V = 384;
 
-struct LinMaps { CUtensorMap m[4]; };
+struct LinMaps { CUtensorMap in[4], out[kLinMaxWalks]; };
 
 struct LinTc {
   LinArgs a;
@@ -66,22 +66,23 @@ struct alignas(1024) LinSmem {
   static constexpr int TILE = C * D * 2;                 // D / 64 blocks of 64 rows of 128 bytes
   uint8_t stage[NST][3][TILE];                           // query | key | value
   uint8_t p[C * 128];                                    // P[i][j], 128-byte swizzle
-  uint16_t o[2][2][C / 2][D];                            // [buffer][half of the tokens]
-  float pw1[2][2 * C];                                   // warps 4-7: A^n at [n], two items alternate
-  float pw2[2][2][C + 8];                                // warps 8-11, 12-15: A^n; [C + 4 ..] hi, lo of A^C and A^tail
+  uint8_t o[2][TILE];                                    // output tiles on their way to memory: 64 rows of 32 channels a warp
+  // tables of the decay, of two items in turn, each group of warps its own:
+  float wv[2][2][2][C];                                  // warps 4-7, 8-11: decay of a token's value in the state behind a
+                                                         // full chunk, and behind the sequence's last one (zeros beyond it)
+  float pz[2][2 * C + 8];                                // warps 12-15: A^n at [C + n], zeros below
+  float wo[2][2][C];                                     // warps 16-19: of the state in a token's output, as wv
   uint64_t full[NST], empty[NST];
-  uint64_t sc_full, p_full, v_full, s_full, u_full, op_full, o_empty, drain;
+  uint64_t sc_full, p_full, v_full, s_full, u_full, u_empty, op_full, o_empty, drain;
   uint32_t taddr;
-  int abort;
 };
 
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, uint32_t* flags, int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (tc::mbar_wait_sleep(bar, parity, flags)) return true;
-  *reinterpret_cast<volatile int*>(abort) = 1;
-  return false;
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
+  return __all_sync(FULL, ltc::wait_tries(bar, parity)) != 0;
 }
-__device__ __forceinline__ bool aborted(const int* abort) { return *reinterpret_cast<const volatile int*>(abort) != 0; }
+__device__ __forceinline__ void gave_up(uint32_t* flags) {
+  if (flags) atomicOr(flags, PACE_FLAG_TIMEOUT);
+}
 
 // Work item: one walk of one stretch of one sequence and head.
 struct Item {
@@ -131,11 +132,10 @@ __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
   for (int x = blockIdx.x; x < t.items && ok; x += gridDim.x) {
     const Item it = item_of<STATE_ONLY>(t, x);
     const bool back = t.a.walk[it.w].back;
-    const CUtensorMap* mp[3] = {&maps.m[t.map_q[it.w]], &maps.m[t.map_k[it.w]], &maps.m[t.map_v[it.w]]};
+    const CUtensorMap* mp[3] = {&maps.in[t.map_q[it.w]], &maps.in[t.map_k[it.w]], &maps.in[t.map_v[it.w]]};
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int s = k % NST, r = k / NST;
-      if (r > 0 && !wait_bar(&sm.empty[s], (uint32_t)((r - 1) & 1), t.a.flags, &sm.abort)) { ok = false; break; }
-      if (aborted(&sm.abort)) { ok = false; break; }
+      if (r > 0 && !ltc::wait_tries(&sm.empty[s], (uint32_t)((r - 1) & 1))) { ok = false; break; }
       const int row = it.begin + chunk_at(it, back, c) * C;
       constexpr int first = STATE_ONLY ? 1 : 0;
       mbar_arrive_expect_tx(&sm.full[s], (3 - first) * SM::TILE);
@@ -146,189 +146,293 @@ __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
           ltc::tensor_load_2d(smem_addr(&sm.stage[s][m][b * C * 128]), mp[m], it.h * D + 64 * b, row, &sm.full[s]);
     }
   }
-  if (!ok) {      // gave up: nothing of ours may land after the block has left
-    for (int j = max(0, k - NST); j < k; ++j)
-      tc::mbar_wait_sleep(&sm.full[j % NST], (uint32_t)((j / NST) & 1), t.a.flags);
+  if (!ok) {
+    gave_up(t.a.flags);
+    // nothing of ours may land after the block has left
+    for (int j = max(0, k - NST); j < k; ++j) ltc::wait_tries(&sm.full[j % NST], (uint32_t)((j / NST) & 1));
   }
 }
 
 // ---- products --------------------------------------------------------------------
+// For each chunk U, then OI, then OP: U's loop (the value's parts into TMEM, U, the parts free again) is the longest of
+// the loops over chunks, and OI waits for the state that comes from the last U.  SC of the next chunk goes as soon as P
+// has been made of this one's.
 template <int D, bool STATE_ONLY>
-__device__ void mma_role(const LinTc& t, LinSmem<D>& sm, uint32_t tm) {
+__device__ void mma_role(const LinTc& t, LinSmem<D>& sm) {
   using SM = LinSmem<D>;
-  constexpr uint32_t id_n64 = ltc::idesc_bf16(128, C, 0), id_u = ltc::idesc_bf16(128, D, 1);
+  constexpr uint32_t id_sc = ltc::idesc_bf16(C, C, 0, 0), id_oi = ltc::idesc_bf16(128, C, 0, 0);
+  constexpr uint32_t id_op = ltc::idesc_bf16(128, C, 1, 0), id_u = ltc::idesc_bf16(128, D, 0, 1);
+  // descriptors of stage 0; a tile or step further is its bytes / 16 more
+  const uint64_t q0 = tc::smem_desc(smem_addr(sm.stage[0][0]), 16, 1024, tc::kSwizzle128);
+  const uint64_t k0 = tc::smem_desc(smem_addr(sm.stage[0][1]), 16, 1024, tc::kSwizzle128);
+  const uint64_t kt0 = tc::smem_desc(smem_addr(sm.stage[0][1]), C * 128, 1024, tc::kSwizzle128);
+  // the value as A has 128 rows; for d = 64 its one block of channels twice, the upper lanes are not read
+  const uint64_t vt0 = tc::smem_desc(smem_addr(sm.stage[0][2]), D == 128 ? C * 128 : 0, 1024, tc::kSwizzle128);
+  const uint64_t p0 = tc::smem_desc(smem_addr(sm.p), 16, 1024, tc::kSwizzle128);
+  constexpr uint32_t kStage = 3 * SM::TILE / 16;
   // this CTA's chunks, over all its items
   int total = 0;
   for (int x = blockIdx.x; x < t.items; x += gridDim.x) total += item_of<STATE_ONLY>(t, x).chunks();
-  auto scores = [&](int k) {
-    const uint32_t q = smem_addr(sm.stage[k % NST][0]), kk = smem_addr(sm.stage[k % NST][1]);
+  auto scores = [&](int s) {
+    if (ltc::elect_one()) {
+#pragma unroll 1
+      for (int b = 0; b < D / 64; ++b) {
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const uint32_t at = (ks >> 2) * (C * 128) + (ks & 3) * 32u;
-      // the product has 128 rows; the tile's 64 are followed by others of the stage, whose lanes nobody reads
-      tc::mma_f16(tm + T_SC, tc::smem_desc(q + at, 16, 1024, tc::kSwizzle128),
-                  tc::smem_desc(kk + at, 16, 1024, tc::kSwizzle128), id_n64, ks > 0);
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint32_t at = kStage * s + b * (C * 8) + ks * 2u;
+          tc::mma_f16(T_SC, q0 + at, k0 + at, id_sc, b + ks > 0);
+        }
+      }
+      tc::commit(&sm.sc_full);
     }
-    tc::commit(&sm.sc_full);
+    __syncwarp();
   };
   bool ok = true;
   if (!STATE_ONLY && total > 0) {
-    ok = wait_bar(&sm.full[0], 0, t.a.flags, &sm.abort);
+    ok = wait_all(&sm.full[0], 0);
     if (ok) scores(0);
   }
+  int s = 0, turn = 0;                       // stage of chunk k and how often the stages went round
   for (int k = 0; k < total && ok; ++k) {
-    const int s = k % NST;
     const uint32_t par = (uint32_t)(k & 1);
-    const uint32_t q = smem_addr(sm.stage[s][0]), kk = smem_addr(sm.stage[s][1]);
-    // the state before the chunk is in TMEM (and the last chunk's U has been read)
-    if (!wait_bar(&sm.s_full, par, t.a.flags, &sm.abort)) break;
-    if (!STATE_ONLY) {
-      if (k > 0 && !wait_bar(&sm.o_empty, par ^ 1u, t.a.flags, &sm.abort)) break;
-      tc::fence_after_sync();
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        ltc::mma_bf16_ta(tm + T_OI, tm + T_S + 8u * ks,
-                         tc::smem_desc(q + (ks >> 2) * (C * 128) + (ks & 3) * 32u, 16, 1024, tc::kSwizzle128), id_n64, ks > 0);
-      if (!wait_bar(&sm.p_full, par, t.a.flags, &sm.abort)) break;
-      if (k + 1 < total) {
-        if (!wait_bar(&sm.full[(k + 1) % NST], (uint32_t)(((k + 1) / NST) & 1), t.a.flags, &sm.abort)) break;
-        tc::fence_after_sync();
-        scores(k + 1);
-      }
-    }
-    if (!wait_bar(&sm.v_full, par, t.a.flags, &sm.abort)) break;
+    const int sn = s + 1 == NST ? 0 : s + 1, turn_n = s + 1 == NST ? turn + 1 : turn;
+    if (!(ok = wait_all(&sm.v_full, par))) break;
+    if (k > 0 && !(ok = wait_all(&sm.u_empty, par ^ 1u))) break;
     tc::fence_after_sync();
+    if (ltc::elect_one()) {
+#pragma unroll 1
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks)
+          ltc::mma_ts(T_U, T_V + 32u * part + 8u * ks, kt0 + (kStage * s + 128u * ks), id_u, part + ks > 0);
+      tc::commit(&sm.u_full);
+      if (STATE_ONLY) tc::commit(&sm.empty[s]);
+    }
+    __syncwarp();
     if (!STATE_ONLY) {
-#pragma unroll
-      for (int ks = 0; ks < C / 16; ++ks)
-        ltc::mma_bf16_ta(tm + T_OP, tm + T_VR + 8u * ks,
-                         tc::smem_desc(smem_addr(sm.p) + ks * 32u, 16, 1024, tc::kSwizzle128), id_n64, ks > 0);
-      tc::commit(&sm.op_full);
-    }
-#pragma unroll
-    for (int part = 0; part < 3; ++part)
-#pragma unroll
-      for (int ks = 0; ks < C / 16; ++ks)
-        ltc::mma_bf16_ta(tm + T_U, tm + T_V + 32u * part + 8u * ks,
-                         tc::smem_desc(kk + ks * 2048u, C * 128, 1024, tc::kSwizzle128), id_u, part + ks > 0);
-    tc::commit(&sm.u_full);
-    tc::commit(&sm.empty[s]);
-  }
-  // every product issued has completed before TMEM is released
-  tc::commit(&sm.drain);
-  tc::mbar_wait_sleep(&sm.drain, 0, t.a.flags);
-}
-
-// ---- P and the value's parts -------------------------------------------------------
-// The value tile, transposed into TMEM lanes: raw, and times its decay in three bf16 parts.
-template <int D, bool TAIL>
-__device__ __forceinline__ void value_parts(const uint8_t* tile, const float* w, int step, int r, uint32_t tm, int e) {
-  // element (token i, channel e): block e / 64, row i, 16-byte piece (e % 64) / 8 exchanged by the row's low bits
-  const uint8_t* base = tile + (e >> 6) * (C * 128) + (e & 7) * 2;
-  const int piece = (e & 63) >> 3;
-  const uint32_t lane_addr = tm + ((uint32_t)(e & ~31) << 16);
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t raw[16], hi[16], mid[16], lo[16];
-#pragma unroll
-    for (int x = 0; x < 16; ++x) {
-      const int i = 32 * half + 2 * x;
-      uint32_t u0 = *reinterpret_cast<const uint16_t*>(base + i * 128 + ((piece ^ (i & 7)) << 4));
-      uint32_t u1 = *reinterpret_cast<const uint16_t*>(base + (i + 1) * 128 + ((piece ^ ((i + 1) & 7)) << 4));
-      if (TAIL) {       // rows behind the sequence's end are somebody else's
-        if (i >= r) u0 = 0;
-        if (i + 1 >= r) u1 = 0;
+      if (!(ok = wait_all(&sm.p_full, par))) break;
+      if (k + 1 < total) {
+        if (!(ok = wait_all(&sm.full[sn], (uint32_t)(turn_n & 1)))) break;
+        tc::fence_after_sync();
+        scores(sn);
       }
-      raw[x] = u0 | (u1 << 16);
-      float x0 = __uint_as_float(u0 << 16), x1 = __uint_as_float(u1 << 16);
-      const float w0 = TAIL ? (i < r ? w[i * step] : 0.f) : w[i * step];
-      const float w1 = TAIL ? (i + 1 < r ? w[(i + 1) * step] : 0.f) : w[(i + 1) * step];
-      x0 *= w0;
-      x1 *= w1;
-      hi[x] = ltc::pack_bf16(x0, x1);
-      x0 -= ltc::bf16_lo(hi[x]);
-      x1 -= ltc::bf16_hi(hi[x]);
-      mid[x] = ltc::pack_bf16(x0, x1);
-      x0 -= ltc::bf16_lo(mid[x]);
-      x1 -= ltc::bf16_hi(mid[x]);
-      lo[x] = ltc::pack_bf16(x0, x1);
+      // the state before the chunk is in TMEM, and the last chunk's output has been read
+      if (!(ok = wait_all(&sm.s_full, par))) break;
+      if (k > 0 && !(ok = wait_all(&sm.o_empty, par ^ 1u))) break;
+      tc::fence_after_sync();
+      if (ltc::elect_one()) {
+#pragma unroll 1
+        for (int b = 0; b < D / 64; ++b)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            ltc::mma_ts(T_OI, T_S + 32u * b + 8u * ks, q0 + (kStage * s + b * (C * 8) + ks * 2u), id_oi, b + ks > 0);
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks)
+          tc::mma_f16(T_OP, vt0 + (kStage * s + 128u * ks), p0 + 2u * ks, id_op, ks > 0);
+        tc::commit(&sm.op_full);
+        tc::commit(&sm.empty[s]);
+      }
+      __syncwarp();
     }
-    ltc::st_32x32b_x16(lane_addr + T_VR + 16u * half, raw);
-    ltc::st_32x32b_x16(lane_addr + T_V + 16u * half, hi);
-    ltc::st_32x32b_x16(lane_addr + T_V + 32u + 16u * half, mid);
-    ltc::st_32x32b_x16(lane_addr + T_V + 64u + 16u * half, lo);
+    s = sn;
+    turn = turn_n;
+  }
+  if (!ok) gave_up(t.a.flags);
+  // every product issued has completed before TMEM is released
+  if (ltc::elect_one()) tc::commit(&sm.drain);
+  __syncwarp();
+  ltc::wait_tries(&sm.drain, 0);
+}
+
+// ---- P, the value's parts, the output -------------------------------------------------
+// These run in short loops on purpose: unrolled, the roles' code was 73 KB and every wait and every step began with
+// instruction cache misses, about 300 cycles each.
+
+// Rows 16 qd .. + 15 of P, from the scores on 16 TMEM lanes of this warp's quadrant.  pz: &sm.pz[..][C], A^n at [n] and
+// zeros below; sgn: 1 forwards, -1 backwards.
+__device__ __forceinline__ void make_p(uint32_t p_smem, const float* pz, int sgn, int r, int qd, int lane) {
+  const int g = lane >> 2, q = lane & 3;
+  // age of (row 16 qd + g, column 8 c + 2 q): sgn (base - 8 c); the next column's is sgn less, and the row 8 below has
+  // the age of the column block before
+  const float* at = pz + sgn * (16 * qd + g - 2 * q + 8);
+  const uint32_t row = 16 * qd + (lane & 15);    // stmatrix: the row whose address this lane gives
+  float2 w0 = make_float2(at[0], at[-sgn]);
+#pragma unroll 1
+  for (int c = 0; c < 8; c += 2) {
+    uint32_t sc[8], m[4];
+    ltc::ld_16x256b_x2(((uint32_t)(32 * qd) << 16) + T_SC + 8 * c, sc);
+    const float2 w1 = make_float2(at[-8 * sgn], at[-9 * sgn]), w2 = make_float2(at[-16 * sgn], at[-17 * sgn]);
+    at -= 16 * sgn;
+    tc::wait_ld();
+    if (r < C) {                                 // scores of keys behind the sequence's end may be anything
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (8 * (c + (x >> 2)) + 2 * q + (x & 1) >= r) sc[x] = 0u;
+    }
+    const float2 w[3] = {w0, w1, w2};
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int x = 4 * y;
+      const float2 a = __fmul2_rn(make_float2(__uint_as_float(sc[x]), __uint_as_float(sc[x + 1])), w[y + 1]);
+      const float2 b = __fmul2_rn(make_float2(__uint_as_float(sc[x + 2]), __uint_as_float(sc[x + 3])), w[y]);
+      m[2 * y] = ltc::pack_bf16(a.x, a.y);
+      m[2 * y + 1] = ltc::pack_bf16(b.x, b.y);
+    }
+    w0 = w2;
+    // matrices: (rows 0-7, block c), (rows 8-15, block c), (rows 0-7, block c + 1), (rows 8-15, block c + 1)
+    ltc::stsm_x4(p_smem + row * 128 + (((c + (lane >> 4)) ^ (row & 7)) << 4), m[0], m[1], m[2], m[3]);
   }
 }
 
+// Tokens 32 th .. + 31 of the value tile, times their decay, transposed for TMEM lanes 32 qd .. + 31 (channels), two
+// tokens a word, in three bf16 parts.  The parts are cut off, not rounded: 8 bits each of the product's 24, so that
+// their sum is the product.  v[part][16 channels of h][..]: words of token groups 0..3, channels g and g + 8.
+__device__ __forceinline__ void value_parts(uint32_t (&v)[3][2][8], uint32_t tile, const float* wv, int r, int th, int qd, int lane) {
+  const int q = lane & 3;
+  // lane's row address of an ldmatrix: matrix lane / 8 = (channels + 8 (m & 1), tokens + 8 (m >> 1)), row lane % 8
+  const int m = lane >> 3, tt = lane & 7;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int ch = 32 * qd + 16 * h + 8 * (m & 1);
+    const uint32_t at = tile + (ch >> 6) * (C * 128) + (32 * th + 8 * (m >> 1) + tt) * 128 + ((((ch & 63) >> 3) ^ tt) << 4);
+    ltc::ldsm_x4_trans(at, v[0][h][0], v[0][h][1], v[0][h][2], v[0][h][3]);
+    ltc::ldsm_x4_trans(at + 2048, v[0][h][4], v[0][h][5], v[0][h][6], v[0][h][7]);
+  }
+  if (r < C) {                                 // rows behind the sequence's end are somebody else's
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int i = 32 * th + 8 * (x >> 1) + 2 * q;
+        v[0][h][x] = i >= r ? 0u : (i + 1 >= r ? v[0][h][x] & 0xffffu : v[0][h][x]);
+      }
+  }
+  const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const float2 w = *reinterpret_cast<const float2*>(wv + 32 * th + 8 * (x >> 1) + 2 * q);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float2 p = __fmul2_rn(make_float2(ltc::bf16_lo(v[0][h][x]), ltc::bf16_hi(v[0][h][x])), w);
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        const uint32_t a0 = __float_as_uint(p.x), a1 = __float_as_uint(p.y);
+        v[part][h][x] = ltc::upper_halves(a0, a1);
+        if (part < 2)
+          p = __ffma2_rn(make_float2(__uint_as_float(a0 & 0xffff0000u), __uint_as_float(a1 & 0xffff0000u)), minus, p);
+      }
+    }
+  }
+  // made here, not behind the wait that follows
+#pragma unroll
+  for (int part = 0; part < 3; ++part)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) asm volatile("" : "+r"(v[part][h][x]));
+}
+
+// The output of a chunk, the 32 channels of this warp's lanes: OP + weight * OI, in 64 rows of 64 bytes of shared memory,
+// whose 16-byte pieces are exchanged as a 64-byte swizzled tensor store wants them.
+template <int D>
+__device__ __forceinline__ void write_out(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, const Item& it, int row, int r,
+                                          const float* wo, int k, int qd, int lane) {
+  tc::fence_after_sync();
+  if (32 * qd < D) {
+    const int q = lane & 3;
+    uint8_t* os = sm.o[k & 1] + qd * (C * 64);
+    if (lane == 0) ltc::bulk_wait_read_1();      // the store of the tile before the last has left this buffer
+    __syncwarp();
+#pragma unroll 1
+    for (int x = 0; x < 4; ++x) {                // 16 channels, 32 tokens: two each of four blocks, channels g and g + 8
+      const int h = x & 1, tq = x >> 1;
+      const uint32_t at = ((uint32_t)(32 * qd + 16 * h) << 16) + 32 * tq;
+      uint32_t oi[16], op[16], m[8];
+      ltc::ld_16x256b_x4(at + T_OI, oi);
+      ltc::ld_16x256b_x4(at + T_OP, op);
+      tc::wait_ld();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float2 wt = *reinterpret_cast<const float2*>(&wo[32 * tq + 8 * b + 2 * q]);
+#pragma unroll
+        for (int y = 2 * b; y < 2 * b + 2; ++y) {
+          const float2 v = __ffma2_rn(make_float2(__uint_as_float(oi[2 * y]), __uint_as_float(oi[2 * y + 1])), wt,
+                                      make_float2(__uint_as_float(op[2 * y]), __uint_as_float(op[2 * y + 1])));
+          m[y] = ltc::pack_bf16(v.x, v.y);
+        }
+      }
+      // matrices: (channels + 0, block b), (+ 8, b), (+ 0, b + 1), (+ 8, b + 1); rows are tokens
+#pragma unroll
+      for (int b = 0; b < 4; b += 2) {
+        const int tok = 32 * tq + 8 * (b + (lane >> 4)) + (lane & 7), piece = 2 * h + ((lane >> 3) & 1);
+        ltc::stsm_x4_trans(smem_addr(os) + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4), m[2 * b], m[2 * b + 1], m[2 * b + 2],
+                           m[2 * b + 3]);
+      }
+    }
+    tc::fence_before_sync();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sm.o_empty);
+    if (r == C) {
+      if (lane == 0) ltc::tensor_store_2d(&maps.out[it.w], smem_addr(os), it.h * D + 32 * qd, row);
+    } else {
+      // the rows behind the end are not ours
+      const LinWalk& w = t.a.walk[it.w];
+      for (int y = lane; y < r * 4; y += 32) {
+        const int i = y >> 2, piece = y & 3;
+        uint16_t* dst = reinterpret_cast<uint16_t*>(w.out) + (size_t)(row + i) * w.out_stride + it.h * D + 32 * qd + 8 * piece;
+        *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(os + i * 64 + ((piece ^ ((i >> 1) & 3)) << 4));
+      }
+    }
+    if (lane == 0) tc::bulk_commit_group();
+  } else if (lane == 0) {
+    tc::mbar_arrive(&sm.o_empty);
+  }
+}
+
+// Warps 4-7 (th = 0) and 8-11 (th = 1): half of the tokens' value parts each.  They are made while U of the chunk before
+// runs and stored when it is done.
 template <int D, bool STATE_ONLY>
-__device__ void value_role(const LinTc& t, LinSmem<D>& sm, uint32_t tm, int warp, int lane) {
-  using SM = LinSmem<D>;
-  const int qd = warp & 3, e = 32 * qd + lane, tid = e;      // e: TMEM lane: value channel, and row i of SC
-  int k = 0, n_item = 0;
+__device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
+  const int qd = warp & 3, th = (warp - 4) >> 2, tid = 32 * qd + lane;
+  int k = 0, n_item = 0, s = 0;
+  uint32_t turn = 0;                             // parity of stage s
   bool ok = true;
   for (int x = blockIdx.x; x < t.items; x += gridDim.x) {
     const Item it = item_of<STATE_ONLY>(t, x);
     if (it.chunks() == 0) continue;
     const bool back = t.a.walk[it.w].back;
-    float* pw = sm.pw1[n_item & 1];
+    float(*wv)[C] = sm.wv[n_item & 1][th];
     ++n_item;
-    const float g = clamp_log_decay(t.a.log_decay[it.h]);
-    if (tid <= C) pw[tid] = decay_pow(g, tid);
-    if (tc::named_sync_any(1, 128, !ok)) return;
-    for (int c = 0; c < it.chunks() && ok; ++c, ++k) {
-      const int s = k % NST, r = it.rows(chunk_at(it, back, c));
-      const uint32_t par = (uint32_t)(k & 1);
-      if (!STATE_ONLY && qd < 2) {
-        // P: rows i on lanes 0..63
-        ok = wait_bar(&sm.sc_full, par, t.a.flags, &sm.abort);
-        if (ok && k > 0) ok = wait_bar(&sm.op_full, par ^ 1u, t.a.flags, &sm.abort);    // the last P has been used
-        if (!__all_sync(FULL, ok)) { ok = false; break; }
-        tc::fence_after_sync();
-        uint8_t* row = sm.p + e * 128;
-#pragma unroll
-        for (int j0 = 0; j0 < C; j0 += 16) {
-          uint32_t sc[16], p2[8];
-          tc::ld_32x32b_x16(tm + ((uint32_t)(32 * qd) << 16) + T_SC + j0, sc);
-          tc::wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float v[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int age = back ? j0 + j + y - e : e - (j0 + j + y);
-              const bool in = age >= 0 && j0 + j + y < r;
-              v[y] = in ? __uint_as_float(sc[j + y]) * pw[age & 63] : 0.f;
-            }
-            p2[j >> 1] = ltc::pack_bf16(v[0], v[1]);
-          }
-          const int ch = j0 >> 3;
-          *reinterpret_cast<uint4*>(row + ((ch ^ (e & 7)) << 4)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-          *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (e & 7)) << 4)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
-        }
-        fence_proxy_async_smem();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.p_full);
-      }
-      ok = wait_bar(&sm.full[s], (uint32_t)((k / NST) & 1), t.a.flags, &sm.abort);
-      if (ok && k > 0) ok = wait_bar(&sm.u_full, par ^ 1u, t.a.flags, &sm.abort);       // the last parts have been used
-      if (!__all_sync(FULL, ok)) { ok = false; break; }
-      tc::fence_after_sync();
+    {
+      // forwards A^(rows - 1 - i), backwards A^(i + 1)
+      const float g = clamp_log_decay(t.a.log_decay[it.h]);
+      const int i = tid & (C - 1), tail = tid >> 6, rows = tail ? it.rows(it.c1 - 1) : C;
+      wv[tail][i] = i < rows ? decay_pow(g, back ? i + 1 : rows - 1 - i) : 0.f;
+    }
+    if (tc::named_sync_any(1 + th, 128, !ok)) break;
+    for (int c = 0; c < it.chunks(); ++c, ++k) {
+      const int r = it.rows(chunk_at(it, back, c));
+      if (!(ok = wait_all(&sm.full[s], turn))) break;
+      uint32_t v[3][2][8];
+      if (32 * qd < D) value_parts(v, smem_addr(sm.stage[s][2]), wv[r < C], r, th, qd, lane);
       if (r < C) {
-        // keys behind the sequence's end: zeros, for their products with zero values must be zero
-        uint8_t* kt = sm.stage[s][1];
+        // keys and values behind the sequence's end: zeros, for products of theirs with zeros must be zero
         for (int y = tid; y < (C - r) * (D / 8); y += 128) {
-          const int row = r + y / (D / 8), ch = y % (D / 8);
-          *reinterpret_cast<uint4*>(kt + (ch >> 3) * (C * 128) + row * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          const int row = r + y / (D / 8), piece = y % (D / 8);
+          *reinterpret_cast<uint4*>(sm.stage[s][1 + th] + (piece >> 3) * (C * 128) + row * 128 + (piece & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
       }
+      if (k > 0 && !(ok = wait_all(&sm.u_full, (uint32_t)((k - 1) & 1)))) break;      // the last chunk's parts have been used
+      tc::fence_after_sync();
       if (32 * qd < D) {
-        // decay of row i: forwards A^(r-1-i), backwards A^(i+1)
-        const float* w = back ? pw + 1 : pw + r - 1;
-        if (r < C) value_parts<D, true>(sm.stage[s][2], w, back ? 1 : -1, r, tm, e);
-        else if (back) value_parts<D, false>(sm.stage[s][2], w, 1, r, tm, e);
-        else value_parts<D, false>(sm.stage[s][2], w, -1, r, tm, e);
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            ltc::st_16x128b_x4(((uint32_t)(32 * qd + 16 * h) << 16) + T_V + 32u * part + 16u * th, v[part][h]);
         ltc::wait_st();
       }
       tc::fence_before_sync();
@@ -337,11 +441,73 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, uint32_t tm, int warp
         tc::mbar_arrive(&sm.v_full);
         tc::mbar_arrive(&sm.empty[s]);
       }
+      if (++s == NST) {
+        s = 0;
+        turn ^= 1u;
+      }
     }
   }
+  if (!ok) gave_up(t.a.flags);
 }
 
-// ---- state and output ---------------------------------------------------------------
+// Warps 12-15: P from the scores.
+template <int D>
+__device__ void score_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
+  const int qd = warp & 3, tid = 32 * qd + lane;
+  int k = 0, n_item = 0;
+  bool ok = true;
+  for (int x = blockIdx.x; x < t.items; x += gridDim.x) {
+    const Item it = item_of<false>(t, x);
+    if (it.chunks() == 0) continue;
+    const bool back = t.a.walk[it.w].back;
+    float* pz = sm.pz[n_item & 1];
+    ++n_item;
+    pz[tid] = tid < C ? 0.f : decay_pow(clamp_log_decay(t.a.log_decay[it.h]), tid - C);
+    if (tid < 8) pz[2 * C + tid] = 0.f;
+    if (tc::named_sync_any(3, 128, !ok)) break;
+    for (int c = 0; c < it.chunks(); ++c, ++k) {
+      if (!(ok = wait_all(&sm.sc_full, (uint32_t)(k & 1)))) break;
+      if (k > 0 && !(ok = wait_all(&sm.op_full, (uint32_t)((k - 1) & 1)))) break;     // the last P has been used
+      tc::fence_after_sync();
+      make_p(smem_addr(sm.p), pz + C, back ? -1 : 1, it.rows(chunk_at(it, back, c)), qd, lane);
+      fence_proxy_async_smem();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.p_full);
+    }
+  }
+  if (!ok) gave_up(t.a.flags);
+}
+
+// Warps 16-19: the outputs.
+template <int D>
+__device__ void out_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, int warp, int lane) {
+  const int qd = warp & 3, tid = 32 * qd + lane;
+  int k = 0, n_item = 0;
+  bool ok = true;
+  for (int x = blockIdx.x; x < t.items; x += gridDim.x) {
+    const Item it = item_of<false>(t, x);
+    if (it.chunks() == 0) continue;
+    const bool back = t.a.walk[it.w].back;
+    float(*wo)[C] = sm.wo[n_item & 1];
+    ++n_item;
+    {
+      // forwards A^(i + 1), backwards A^(rows - 1 - i)
+      const int i = tid & (C - 1), rows = tid < C ? C : it.rows(it.c1 - 1);
+      wo[tid >> 6][i] = decay_pow(clamp_log_decay(t.a.log_decay[it.h]), back ? max(rows - 1 - i, 0) : i + 1);
+    }
+    if (tc::named_sync_any(4, 128, !ok)) break;
+    for (int c = 0; c < it.chunks(); ++c, ++k) {
+      const int ch = chunk_at(it, back, c), r = it.rows(ch);
+      if (!(ok = wait_all(&sm.op_full, (uint32_t)(k & 1)))) break;
+      write_out<D>(t, maps, sm, it, it.begin + ch * C, r, wo[r < C], k, qd, lane);
+    }
+  }
+  if (lane == 0) tc::bulk_wait_all();
+  if (!ok) gave_up(t.a.flags);
+}
+
+// ---- state ---------------------------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void state_to_tmem(const float (&S)[D / 2], uint32_t at) {
 #pragma unroll
@@ -355,16 +521,15 @@ __device__ __forceinline__ void state_to_tmem(const float (&S)[D / 2], uint32_t 
 }
 
 template <int D, bool STATE_ONLY>
-__device__ void state_role(const LinTc& t, LinSmem<D>& sm, uint32_t tm, int warp, int lane) {
+__device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   constexpr int HC = D / 2;                                  // key channels of a thread
-  const int qd = warp & 3, half = (warp - 8) >> 2, e = 32 * qd + lane, tid = e;
+  const int qd = warp & 3, half = (warp - 20) >> 2, e = 32 * qd + lane;
   const bool mine = 32 * qd < D;                             // lanes beyond d hold nothing
-  const uint32_t lane_addr = tm + ((uint32_t)(32 * qd) << 16);
-  const int bar_id = 2 + half;
-  int k = 0, n_item = 0;
+  const uint32_t lane_addr = (uint32_t)(32 * qd) << 16;
+  int k = 0;
   bool ok = true;
   float S[HC];
-  for (int x = blockIdx.x; x < t.items; x += gridDim.x) {
+  for (int x = blockIdx.x; x < t.items && ok; x += gridDim.x) {
     const Item it = item_of<STATE_ONLY>(t, x);
     if (!it.on) continue;
     const LinWalk& w = t.a.walk[it.w];
@@ -375,17 +540,6 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, uint32_t tm, int warp
     float* out = STATE_ONLY ? stretch_state(t, it)
                             : (w.S_out && it.seg == (back ? 0 : it.nseg - 1) ? w.S_out + st0 : nullptr);
     const bool out_swap = !STATE_ONLY && w.swap != 0;
-    // tables of the decay
-    float* pw = sm.pw2[n_item & 1][half];
-    ++n_item;
-    const float g = clamp_log_decay(t.a.log_decay[it.h]);
-    if (tid < C) pw[tid] = decay_pow(g, tid + (back ? 0 : 1));        // forwards A^(i+1); backwards A^i
-    if (tid >= 96 && tid < 98 && it.chunks() > 0) {
-      // A^rows of a full chunk and of the last one, 48 bits: the state is multiplied by them all along
-      const double a = exp((double)g * (tid == 96 ? C : it.rows(it.c1 - 1)));
-      pw[C + 4 + 2 * (tid - 96)] = (float)a;
-      pw[C + 5 + 2 * (tid - 96)] = (float)(a - (double)(float)a);
-    }
     if (mine) {
       if (in && in_swap) {
 #pragma unroll
@@ -399,84 +553,66 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, uint32_t tm, int warp
         for (int j = 0; j < HC; ++j) S[j] = 0.f;
       }
     }
-    if (tc::named_sync_any(bar_id, 128, !ok)) return;
+    // A^rows - 1: S + (A^rows - 1) S keeps what a product with A^rows, rounded to 24 bits, would lose chunk after chunk
+    const float g = clamp_log_decay(t.a.log_decay[it.h]);
+    const float lost_full = expm1f(g * C), lost_tail = it.chunks() > 0 ? expm1f(g * (float)it.rows(it.c1 - 1)) : 0.f;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
-      const int ch = chunk_at(it, back, c), r = it.rows(ch);
+      const int r = it.rows(chunk_at(it, back, c));
       const uint32_t par = (uint32_t)(k & 1);
-      if (c == 0) {
-        // the state before the first chunk; the products of the chunk before have been waited for
-        if (!STATE_ONLY && mine) state_to_tmem<D>(S, lane_addr + T_S + (HC / 2) * half);
+      if (c == 0 && !STATE_ONLY) {
+        // the state before the first chunk; the last item's products have been waited for
+        if (mine) state_to_tmem<D>(S, lane_addr + T_S + (HC / 2) * half);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.s_full);
       }
-      ok = __all_sync(FULL, wait_bar(&sm.u_full, par, t.a.flags, &sm.abort));
-      if (ok) {
-        tc::fence_after_sync();
-        const float ah = pw[C + 4 + (r < C ? 2 : 0)], al = pw[C + 5 + (r < C ? 2 : 0)];
-        if (mine) {
-          const float2 h2 = make_float2(ah, ah), l2 = make_float2(al, al);
+      if (mine) {        // while U runs
+        const float m = r < C ? lost_tail : lost_full;
+        const float2 m2 = make_float2(m, m);
 #pragma unroll
-          for (int j0 = 0; j0 < HC; j0 += 16) {
-            uint32_t u[16];
-            tc::ld_32x32b_x16(lane_addr + T_U + HC * half + j0, u);
-            tc::wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const float2 s2 = make_float2(S[j0 + j], S[j0 + j + 1]);
-              const float2 n2 = __ffma2_rn(s2, h2, __ffma2_rn(s2, l2, make_float2(__uint_as_float(u[j]), __uint_as_float(u[j + 1]))));
-              S[j0 + j] = n2.x;
-              S[j0 + j + 1] = n2.y;
-            }
-          }
+        for (int j = 0; j < HC; j += 2) {
+          const float2 s2 = make_float2(S[j], S[j + 1]), n2 = __ffma2_rn(s2, m2, s2);
+          S[j] = n2.x;
+          S[j + 1] = n2.y;
         }
-        if (c + 1 < it.chunks()) {
-          if (!STATE_ONLY && mine) state_to_tmem<D>(S, lane_addr + T_S + (HC / 2) * half);
+#pragma unroll
+        for (int j = 0; j < HC; ++j) asm volatile("" : "+f"(S[j]));
+      }
+      if (!(ok = wait_all(&sm.u_full, par))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int j0 = 0; j0 < HC; j0 += 16) {
+        uint32_t u[16];
+        if (mine) {
+          tc::ld_32x32b_x16(lane_addr + T_U + HC * half + j0, u);
+          tc::wait_ld();
+        }
+        if (j0 + 16 == HC) {         // U may be written again
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.s_full);
+          if (lane == 0) tc::mbar_arrive(&sm.u_empty);
         }
-      }
-      if (STATE_ONLY) {
-        if (tc::named_sync_any(bar_id, 128, !ok)) return;
-        continue;
-      }
-      // the output: tokens 32 half .. + 31 of the chunk
-      if (ok) ok = __all_sync(FULL, wait_bar(&sm.op_full, par, t.a.flags, &sm.abort));
-      uint16_t(*os)[D] = sm.o[k & 1][half];
-      if (ok) {
-        tc::fence_after_sync();
         if (mine) {
 #pragma unroll
-          for (int i0 = 0; i0 < 32; i0 += 16) {
-            uint32_t oi[16], op[16];
-            tc::ld_32x32b_x16(lane_addr + T_OI + 32 * half + i0, oi);
-            tc::ld_32x32b_x16(lane_addr + T_OP + 32 * half + i0, op);
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int tok = 32 * half + i0 + i;
-              const float wt = back ? pw[max(r - 1 - tok, 0)] : pw[tok];
-              os[i0 + i][e] = float_to_bf16_bits_rn(fmaf(wt, __uint_as_float(oi[i]), __uint_as_float(op[i])));
-            }
+          for (int j = 0; j < 16; j += 2) {
+            const float2 n2 = __fadd2_rn(make_float2(S[j0 + j], S[j0 + j + 1]),
+                                         make_float2(__uint_as_float(u[j]), __uint_as_float(u[j + 1])));
+            S[j0 + j] = n2.x;
+            S[j0 + j + 1] = n2.y;
           }
         }
+      }
+      if (STATE_ONLY) continue;
+      if (!(ok = wait_all(&sm.op_full, par))) break;          // the last copy has been used
+      if (c + 1 < it.chunks()) {
+        tc::fence_after_sync();
+        if (mine) state_to_tmem<D>(S, lane_addr + T_S + (HC / 2) * half);
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.o_empty);
-      }
-      if (tc::named_sync_any(bar_id, 128, !ok)) return;
-      constexpr int PR = D / 8;                              // 16-byte pieces a row
-#pragma unroll
-      for (int y = tid; y < 32 * PR; y += 128) {
-        const int i = y / PR, ch16 = y % PR, tok = 32 * half + i;
-        if (tok < r) {
-          uint16_t* dst = reinterpret_cast<uint16_t*>(w.out) + (size_t)(it.begin + ch * C + tok) * w.out_stride + it.h * D + 8 * ch16;
-          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(&os[i][8 * ch16]);
-        }
+        if (lane == 0) tc::mbar_arrive(&sm.s_full);
       }
     }
-    if (out && mine) {
+    if (out && mine && ok) {
       if (out_swap) {
 #pragma unroll
         for (int j = 0; j < HC; ++j) out[(size_t)(HC * half + j) * D + e] = S[j];
@@ -487,6 +623,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, uint32_t tm, int warp
       }
     }
   }
+  if (!ok) gave_up(t.a.flags);
 }
 
 template <int D, bool STATE_ONLY>
@@ -499,39 +636,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 5);              // the products, and the four warps that read the values
+      mbar_init(&sm.empty[s], 9);              // the products, and the eight warps that read the values
     }
     mbar_init(&sm.sc_full, 1);
-    mbar_init(&sm.p_full, 2);
-    mbar_init(&sm.v_full, 4);
+    mbar_init(&sm.p_full, 4);
+    mbar_init(&sm.v_full, 8);
     mbar_init(&sm.s_full, 8);
     mbar_init(&sm.u_full, 1);
+    mbar_init(&sm.u_empty, 8);
     mbar_init(&sm.op_full, 1);
-    mbar_init(&sm.o_empty, 8);
+    mbar_init(&sm.o_empty, 4);
     mbar_init(&sm.drain, 1);
-    sm.abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(&sm.taddr, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tm = sm.taddr;
-  if (warp == 0) {
-    if (lane == 0) load_role<D, STATE_ONLY>(t, maps, sm);
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) mma_role<D, STATE_ONLY>(t, sm, tm);
-    __syncwarp();
-  } else if (warp >= 8) {
-    state_role<D, STATE_ONLY>(t, sm, tm, warp, lane);
-  } else if (warp >= 4) {
-    value_role<D, STATE_ONLY>(t, sm, tm, warp, lane);
+  // registers: 896 threads x 72 at launch hold 128 x (40 + 72 + 72 + 48 + 56 + 104 + 104)
+  if (warp < 4) {
+    ltc::regs_down<40>();
+    if (warp == 0) {
+      if (lane == 0) load_role<D, STATE_ONLY>(t, maps, sm);
+      __syncwarp();
+    } else if (warp == 1) {
+      mma_role<D, STATE_ONLY>(t, sm);
+    }
+  } else if (warp < 12) {
+    value_role<D, STATE_ONLY>(t, sm, warp, lane);
+  } else if (warp < 16) {
+    ltc::regs_down<48>();
+    if (!STATE_ONLY) score_role<D>(t, sm, warp, lane);
+  } else if (warp < 20) {
+    ltc::regs_down<56>();
+    if (!STATE_ONLY) out_role<D>(t, maps, sm, warp, lane);
+  } else {
+    ltc::regs_up<104>();
+    state_role<D, STATE_ONLY>(t, sm, warp, lane);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_free(tm, 512);
+  if (warp == 1) tc::tmem_free(sm.taddr, 512);
 }
 
 // ---- chaining the stretches ----------------------------------------------------------
@@ -603,16 +749,16 @@ EncodeFn encode_fn() {
   return encode;
 }
 
-// rows of `width` bf16, `stride` elements apart, in boxes of 64 rows of 64 elements
-bool make_map(CUtensorMap* m, const void* p, int64_t width, int64_t stride, int64_t rows) {
+// rows of `width` bf16, `stride` elements apart, in boxes of 64 rows of `inner` (64 or 32) elements
+bool make_map(CUtensorMap* m, const void* p, int64_t width, int64_t stride, int64_t rows, int inner) {
   EncodeFn encode = encode_fn();
   if (!encode) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)C};
+  const cuuint32_t box[2] = {(cuuint32_t)inner, (cuuint32_t)C};
   const cuuint32_t estr[2] = {1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -678,7 +824,7 @@ cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, c
   auto index = [&](const void* p, int64_t stride) {
     for (int i = 0; i < n; ++i)
       if (seen[i].p == p && seen[i].stride == stride) return i;
-    if (n == 4 || !make_map(&maps.m[n], p, (int64_t)a.H * a.D, stride, a.total)) return -1;
+    if (n == 4 || !make_map(&maps.in[n], p, (int64_t)a.H * a.D, stride, a.total, 64)) return -1;
     seen[n] = Seen{p, stride};
     return n++;
   };
@@ -687,6 +833,7 @@ cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, c
     t.map_k[w] = index(a.walk[w].key, a.walk[w].key_stride);
     t.map_v[w] = index(a.walk[w].value, a.walk[w].value_stride);
     if (t.map_q[w] < 0 || t.map_k[w] < 0 || t.map_v[w] < 0) return cudaErrorInvalidValue;
+    if (!make_map(&maps.out[w], a.walk[w].out, (int64_t)a.H * a.D, a.walk[w].out_stride, a.total, 32)) return cudaErrorInvalidValue;
   }
   return a.D == 128 ? launch_tc<128>(t, maps, st) : launch_tc<64>(t, maps, st);
 }
