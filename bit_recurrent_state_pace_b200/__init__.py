@@ -407,23 +407,52 @@ def _plain(name: str, t: Optional[torch.Tensor], shape, dtype, like: torch.Tenso
     return t.data_ptr()
 
 
-class _On:
-    """Makes a tensor's device current for a call and gives the stream to launch on."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # current_stream() without the wrapper object
 
-    def __init__(self, t: torch.Tensor, stream):
-        self.index = t.device.index
+
+class _On:
+    """Makes a device current for a call and gives the stream to launch on."""
+    __slots__ = ("index", "stream", "back")
+
+    def __init__(self, index: int, stream):
+        self.index = index
         self.stream = stream
 
     def __enter__(self):
         self.back = torch.cuda.current_device()
         if self.back != self.index:
             torch.cuda.set_device(self.index)
+        if self.stream is None and _raw_stream is not None:
+            return _raw_stream(self.index)
         return _stream(self.stream)
 
     def __exit__(self, *exc):
         if self.back != self.index:
             torch.cuda.set_device(self.back)
         return False
+
+
+# What a call's shapes, strides, types and devices lead to (the checks passed, the descriptor, sizes), kept so that
+# the next call of the same form pays for a lookup; no tensor and no address is kept.
+_plans: dict = {}
+
+
+def _form(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _plan(key, build):
+    plan = _plans.get(key)
+    if plan is None:
+        plan = build()
+        if len(_plans) >= 4096:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
+def _opt(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -477,6 +506,17 @@ def pace_linattn_workspace_bytes(num_seqs: int, num_heads: int, d: int, io: int,
     return n.value
 
 
+def _tensors(*named) -> None:
+    for name, t in named:
+        _need(t is None or (isinstance(t, torch.Tensor) and t.is_cuda), f"{name}: a device tensor")
+
+
+def _lin_workspace(fn: str, desc, backward: int) -> int:
+    size = ctypes.c_size_t()
+    _check(fn, lib.pace_linattn_workspace_bytes(ctypes.byref(desc), backward, ctypes.byref(size)))
+    return size.value
+
+
 def pace_linattn_forward(q, k, v, log_decay, o=None, ST=None, num_seqs=None, max_len=None, cu_seqlens=None, S0=None,
                          workspace=None, flags=None, stream=None, need_ST=True):
     """Linear attention with a fixed decay for each head over prompts: returns (o, ST).
@@ -485,25 +525,32 @@ def pace_linattn_forward(q, k, v, log_decay, o=None, ST=None, num_seqs=None, max
     cu_seqlens: int32 [N + 1], or None for prompts of one length; S0, ST: fp32 [N, H, d, d].  Rows of no sequence
     are left as they are (unset in an o made here).
     """
-    desc, total, n, H, d = _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens)
+    _tensors(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("o", o), ("ST", ST), ("cu_seqlens", cu_seqlens),
+             ("S0", S0), ("flags", flags))
+
+    def build():
+        desc, total, n, H, d = _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens)
+        if o is not None:
+            to, desc.o_stride = _rows("o", o, H, d, q)
+            _need(to == total, "o: as many rows as q")
+        _plain("log_decay", log_decay, (H,), torch.float32, q)
+        _plain("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, q)
+        _plain("S0", S0, (n, H, d, d), torch.float32, q)
+        _plain("ST", ST, (n, H, d, d), torch.float32, q)
+        _plain("flags", flags, (1,), torch.int32, q)
+        return desc, ctypes.byref(desc), (n, H, d, d), _lin_workspace("pace_linattn_forward", desc, 0)
+
+    desc, ref, states, size = _plan(("fwd", _form(q), _form(k), _form(v), _form(log_decay), _form(o), _form(ST),
+                                     _form(cu_seqlens), _form(S0), _form(flags), num_seqs, max_len), build)
     if o is None:
         o = _new(q.shape, q.dtype, q, stream)
-    to, desc.o_stride = _rows("o", o, H, d, q)
-    _need(to == total, "o: as many rows as q")
     if ST is None and need_ST:
-        ST = _new((n, H, d, d), torch.float32, q, stream)
-    g = _plain("log_decay", log_decay, (H,), torch.float32, q)
-    cu = _plain("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, q)
-    s0 = _plain("S0", S0, (n, H, d, d), torch.float32, q)
-    st = _plain("ST", ST, (n, H, d, d), torch.float32, q)
-    fl = _plain("flags", flags, (1,), torch.int32, q)
-    size = ctypes.c_size_t()
-    _check("pace_linattn_forward", lib.pace_linattn_workspace_bytes(ctypes.byref(desc), 0, ctypes.byref(size)))
-    ws = _workspace("pace_linattn_forward", size.value, workspace, q, stream)
-    with _On(q, stream) as s:
+        ST = _new(states, torch.float32, q, stream)
+    ws = _workspace("pace_linattn_forward", size, workspace, q, stream)
+    with _On(q.device.index, stream) as s:
         _check("pace_linattn_forward", lib.pace_linattn_forward(
-            ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), g, cu, s0, o.data_ptr(), st,
-            None if ws is None else ws.data_ptr(), fl, s))
+            ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _opt(cu_seqlens), _opt(S0), o.data_ptr(),
+            _opt(ST), _opt(ws), _opt(flags), s))
     return o, ST
 
 
@@ -513,59 +560,72 @@ def pace_linattn_backward(q, k, v, log_decay, d_o, dq=None, dk=None, dv=None, dS
 
     dq, dk, dv have the row strides of q, k, v; those not given are made so (rows of no sequence are left unset).
     """
-    desc, total, n, H, d = _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens)
-    to, desc.o_stride = _rows("d_o", d_o, H, d, q)
-    _need(to == total, "d_o: as many rows as q")
+    _tensors(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("d_o", d_o), ("dq", dq), ("dk", dk), ("dv", dv),
+             ("dS0", dS0), ("cu_seqlens", cu_seqlens), ("S0", S0), ("dST", dST), ("flags", flags))
+
+    def build():
+        desc, total, n, H, d = _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens)
+        to, desc.o_stride = _rows("d_o", d_o, H, d, q)
+        _need(to == total, "d_o: as many rows as q")
+        rooms = []               # elements to make a strided gradient in; None: packed
+        for name, given, stride in (("dq", dq, desc.q_stride), ("dk", dk, desc.k_stride), ("dv", dv, desc.v_stride)):
+            rooms.append(None if stride in (0, H * d) else max(total, 1) * stride)
+            if given is not None:
+                tg, sg = _rows(name, given, H, d, q)
+                _need(tg == total and (total <= 1 or (sg or H * d) == (stride or H * d)), f"{name}: rows as those of {name[1:]}")
+        _plain("log_decay", log_decay, (H,), torch.float32, q)
+        _plain("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, q)
+        _plain("S0", S0, (n, H, d, d), torch.float32, q)
+        _plain("dST", dST, (n, H, d, d), torch.float32, q)
+        _plain("dS0", dS0, (n, H, d, d), torch.float32, q)
+        _plain("flags", flags, (1,), torch.int32, q)
+        return desc, ctypes.byref(desc), (n, H, d, d), rooms, _lin_workspace("pace_linattn_backward", desc, 1)
+
+    desc, ref, states, rooms, size = _plan(
+        ("bwd", _form(q), _form(k), _form(v), _form(log_decay), _form(d_o), _form(dq), _form(dk), _form(dv), _form(dS0),
+         _form(cu_seqlens), _form(S0), _form(dST), _form(flags), num_seqs, max_len), build)
     made = []
-    for name, given, like, stride in (("dq", dq, q, desc.q_stride), ("dk", dk, k, desc.k_stride),
-                                      ("dv", dv, v, desc.v_stride)):
+    for given, like, room in ((dq, q, rooms[0]), (dk, k, rooms[1]), (dv, v, rooms[2])):
         if given is None:
-            if stride in (0, H * d):
-                given = _new(like.shape, like.dtype, q, stream)
-            else:
-                room = _new(max(total, 1) * stride, like.dtype, q, stream)
-                given = room.as_strided(like.shape, like.stride())
-        tg, sg = _rows(name, given, H, d, q)
-        _need(tg == total and (total <= 1 or (sg or H * d) == (stride or H * d)), f"{name}: rows as those of {name[1:]}")
+            given = (_new(like.shape, like.dtype, q, stream) if room is None
+                     else _new(room, like.dtype, q, stream).as_strided(like.shape, like.stride()))
         made.append(given)
     dq, dk, dv = made
     if dS0 is None and (S0 is not None if need_dS0 is None else need_dS0):
-        dS0 = _new((n, H, d, d), torch.float32, q, stream)
-    g = _plain("log_decay", log_decay, (H,), torch.float32, q)
-    cu = _plain("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, q)
-    s0 = _plain("S0", S0, (n, H, d, d), torch.float32, q)
-    dst = _plain("dST", dST, (n, H, d, d), torch.float32, q)
-    ds0 = _plain("dS0", dS0, (n, H, d, d), torch.float32, q)
-    fl = _plain("flags", flags, (1,), torch.int32, q)
-    size = ctypes.c_size_t()
-    _check("pace_linattn_backward", lib.pace_linattn_workspace_bytes(ctypes.byref(desc), 1, ctypes.byref(size)))
-    ws = _workspace("pace_linattn_backward", size.value, workspace, q, stream)
-    with _On(q, stream) as s:
+        dS0 = _new(states, torch.float32, q, stream)
+    ws = _workspace("pace_linattn_backward", size, workspace, q, stream)
+    with _On(q.device.index, stream) as s:
         _check("pace_linattn_backward", lib.pace_linattn_backward(
-            ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), g, cu, s0, d_o.data_ptr(), dst,
-            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ds0, None if ws is None else ws.data_ptr(), fl, s))
+            ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _opt(cu_seqlens), _opt(S0), d_o.data_ptr(),
+            _opt(dST), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _opt(dS0), _opt(ws), _opt(flags), s))
     return dq, dk, dv, dS0
 
 
 def pace_linattn_step(S, q, k, v, log_decay, o=None, stream=None) -> torch.Tensor:
     """One token for each of N sequences: q, k, v [N, H, d]; S fp32 [N, H, d, d] is updated in place; returns o."""
-    _need(isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3, "q: device tensor [N, H, d]")
-    _need(q.dtype in _IO_OF, f"q: bfloat16 or float32, not {q.dtype}")
-    n, H, d = q.shape
+    _tensors(("S", S), ("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("o", o))
+
+    def build():
+        _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q: device tensor [N, H, d]")
+        _need(q.dtype in _IO_OF, f"q: bfloat16 or float32, not {q.dtype}")
+        n, H, d = q.shape
+        strides = []
+        for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
+            rows, st = (n, 0) if name == "o" and t is None else _rows(name, t, H, d, q)
+            _need(rows == n, f"{name}: {n} rows")
+            strides.append(st)
+        _need(S is not None, "S: the states")
+        _plain("S", S, (n, H, d, d), torch.float32, q)
+        _plain("log_decay", log_decay, (H,), torch.float32, q)
+        desc = _LinattnDesc(n, H, d, d, _IO_OF[q.dtype], 0, 0, *strides)
+        return desc, ctypes.byref(desc)
+
+    _, ref = _plan(("step", _form(S), _form(q), _form(k), _form(v), _form(log_decay), _form(o)), build)
     if o is None:
         o = _new(q.shape, q.dtype, q, stream)
-    strides = []
-    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
-        rows, st = _rows(name, t, H, d, q)
-        _need(rows == n, f"{name}: {n} rows")
-        strides.append(st)
-    _need(S is not None, "S: the states")
-    sp = _plain("S", S, (n, H, d, d), torch.float32, q)
-    g = _plain("log_decay", log_decay, (H,), torch.float32, q)
-    desc = _LinattnDesc(n, H, d, d, _IO_OF[q.dtype], 0, 0, *strides)
-    with _On(q, stream) as s:
-        _check("pace_linattn_step", lib.pace_linattn_step(ctypes.byref(desc), sp, q.data_ptr(), k.data_ptr(),
-                                                          v.data_ptr(), g, o.data_ptr(), s))
+    with _On(q.device.index, stream) as s:
+        _check("pace_linattn_step", lib.pace_linattn_step(ref, S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                                          log_decay.data_ptr(), o.data_ptr(), s))
     return o
 
 
@@ -573,9 +633,9 @@ _NORM_OF = {"l2": PACE_NORM_L2, "rms": PACE_NORM_RMS, PACE_NORM_L2: PACE_NORM_L2
 
 
 def _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved, norm, eps, q_scale):
-    """Descriptor (strides of q and k set) and the addresses of weights, positions and frequencies."""
+    """Descriptor (strides of q and k set), the tensor that gives type and device, heads, rows and d."""
     like = q if q is not None else k
-    _need(isinstance(like, torch.Tensor) and like.is_cuda and like.dim() >= 3, "q or k: device tensor [..., heads, d]")
+    _need(isinstance(like, torch.Tensor) and like.dim() >= 3, "q or k: device tensor [..., heads, d]")
     _need(like.dtype in _IO_OF, f"q, k: bfloat16 or float32, not {like.dtype}")
     _need(norm in _NORM_OF, "norm: 'l2' or 'rms'")
     d = like.shape[-1]
@@ -592,16 +652,13 @@ def _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interlea
     if rotary_dim:
         _need(positions is not None and inv_freq is not None, "positions and inv_freq: given with rotary_dim")
     _need(positions is None or positions.numel() == rows[0], f"positions: {rows[0]} of them")
-    ptrs = (_plain("q_weight", q_weight, (d,), torch.float32, like), _plain("k_weight", k_weight, (d,), torch.float32, like),
-            _plain("positions", positions, () if positions is None else positions.shape, torch.int32, like),
-            _plain("inv_freq", inv_freq, (half,), torch.float32, like))
+    _plain("q_weight", q_weight, (d,), torch.float32, like)
+    _plain("k_weight", k_weight, (d,), torch.float32, like)
+    _plain("positions", positions, () if positions is None else positions.shape, torch.int32, like)
+    _plain("inv_freq", inv_freq, (half,), torch.float32, like)
     desc = _QkNormDesc(rows[0], heads[0], heads[1], d, int(rotary_dim), int(bool(interleaved)), _NORM_OF[norm],
                        _IO_OF[like.dtype], float(eps), float(q_scale), strides[0], strides[1], 0, 0)
-    return desc, like, heads, rows[0], d, ptrs
-
-
-def _opt(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+    return desc, like, heads, rows[0], d
 
 
 def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, q_out=None, k_out=None,
@@ -610,25 +667,34 @@ def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_
 
     q: [tokens, Hq, d], k: [tokens, Hk, d] (either may be None); q_out may be q, k_out may be k.
     """
-    desc, like, heads, rows, d, ptrs = _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved,
-                                                norm, eps, q_scale)
-    outs = []
-    for i, (name, t, x) in enumerate((("q_out", q_out, q), ("k_out", k_out, k))):
-        _need(x is not None or t is None, f"{name}: given without its input")
-        if x is not None:
+    _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),
+             ("inv_freq", inv_freq), ("q_out", q_out), ("k_out", k_out))
+
+    def build():
+        desc, like, heads, rows, d = _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved, norm,
+                                              eps, q_scale)
+        for i, (name, t, x) in enumerate((("q_out", q_out, q), ("k_out", k_out, k))):
+            _need(x is not None or t is None, f"{name}: given without its input")
             if t is None:
-                t = _new(x.shape, x.dtype, like, stream)
+                continue
             n, st = _rows(name, t, heads[i], d, like)
             _need(n == rows, f"{name}: {rows} rows")
             if i:
                 desc.k_out_stride = st
             else:
                 desc.q_out_stride = st
-        outs.append(t)
-    with _On(like, stream) as s:
-        _check("pace_qk_norm_rotate", lib.pace_qk_norm_rotate(ctypes.byref(desc), _opt(q), _opt(k), *ptrs, _opt(outs[0]),
-                                                              _opt(outs[1]), s))
-    return tuple(outs)
+        return desc, ctypes.byref(desc)
+
+    _, ref = _plan(("norm", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq),
+                    _form(q_out), _form(k_out), rotary_dim, interleaved, norm, eps, q_scale), build)
+    if q_out is None and q is not None:
+        q_out = _new(q.shape, q.dtype, q, stream)
+    if k_out is None and k is not None:
+        k_out = _new(k.shape, k.dtype, k, stream)
+    with _On((q if q is not None else k).device.index, stream) as s:
+        _check("pace_qk_norm_rotate", lib.pace_qk_norm_rotate(
+            ref, _opt(q), _opt(k), _opt(q_weight), _opt(k_weight), _opt(positions), _opt(inv_freq), _opt(q_out), _opt(k_out), s))
+    return q_out, k_out
 
 
 def pace_qk_norm_workspace_bytes(num_tokens: int, num_q_heads: int, num_k_heads: int, head_dim: int, io: int) -> int:
@@ -643,40 +709,54 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
                                  q_scale=1.0, workspace=None, stream=None):
     """Gradients of pace_qk_norm_rotate: returns (dq, dk, dq_weight, dk_weight); a weight's gradient is made where the
     weight is given (or a tensor for it)."""
-    desc, like, heads, rows, d, ptrs = _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved,
-                                                norm, eps, q_scale)
-    outs, grads, dws = [], [], []
-    for i, (x, dy, dx, w, dw) in enumerate(((q, d_q_out, dq, q_weight, dq_weight), (k, d_k_out, dk, k_weight, dk_weight))):
-        name = "qk"[i]
-        _need((x is None) == (dy is None), f"d_{name}_out: given with {name}")
-        if x is None:
-            _need(dx is None and dw is None, f"d{name}: given without {name}")
-            outs.append(None), grads.append(None), dws.append(None)
-            continue
-        n, st = _rows(f"d_{name}_out", dy, heads[i], d, like)
-        _need(n == rows and (n <= 1 or st in (0, heads[i] * d)), f"d_{name}_out: {rows} packed rows")
-        if dx is None:
-            dx = _new(x.shape, x.dtype, like, stream)
-        n, st = _rows(f"d{name}", dx, heads[i], d, like)
-        _need(n == rows, f"d{name}: {rows} rows")
-        if i:
-            desc.k_out_stride = st
-        else:
-            desc.q_out_stride = st
-        if dw is None and w is not None:
-            dw = _new((d,), torch.float32, like, stream)
-        outs.append(dx), grads.append(dy), dws.append(dw)
-    dwp = [_plain("dq_weight", dws[0], (d,), torch.float32, like), _plain("dk_weight", dws[1], (d,), torch.float32, like)]
-    ws = None
-    if dwp[0] is not None or dwp[1] is not None:
+    _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),
+             ("inv_freq", inv_freq), ("d_q_out", d_q_out), ("d_k_out", d_k_out), ("dq", dq), ("dk", dk),
+             ("dq_weight", dq_weight), ("dk_weight", dk_weight))
+
+    def build():
+        desc, like, heads, rows, d = _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved, norm,
+                                              eps, q_scale)
+        for i, (x, dy, dx, dw) in enumerate(((q, d_q_out, dq, dq_weight), (k, d_k_out, dk, dk_weight))):
+            name = "qk"[i]
+            _need((x is None) == (dy is None), f"d_{name}_out: given with {name}")
+            if x is None:
+                _need(dx is None and dw is None, f"d{name}: given without {name}")
+                continue
+            n, st = _rows(f"d_{name}_out", dy, heads[i], d, like)
+            _need(n == rows and (n <= 1 or st in (0, heads[i] * d)), f"d_{name}_out: {rows} packed rows")
+            if dx is not None:
+                n, st = _rows(f"d{name}", dx, heads[i], d, like)
+                _need(n == rows, f"d{name}: {rows} rows")
+                if i:
+                    desc.k_out_stride = st
+                else:
+                    desc.q_out_stride = st
+            _plain(f"d{name}_weight", dw, (d,), torch.float32, like)
         size = ctypes.c_size_t()
         _check("pace_qk_norm_rotate_backward", lib.pace_qk_norm_workspace_bytes(ctypes.byref(desc), ctypes.byref(size)))
-        ws = _workspace("pace_qk_norm_rotate_backward", size.value, workspace, like, stream)
-    with _On(like, stream) as s:
+        return desc, ctypes.byref(desc), (d,), size.value
+
+    _, ref, wide, size = _plan(
+        ("normb", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq), _form(d_q_out),
+         _form(d_k_out), _form(dq), _form(dk), _form(dq_weight), _form(dk_weight), rotary_dim, interleaved, norm, eps,
+         q_scale), build)
+    like = q if q is not None else k
+    if dq is None and q is not None:
+        dq = _new(q.shape, q.dtype, q, stream)
+    if dk is None and k is not None:
+        dk = _new(k.shape, k.dtype, k, stream)
+    if dq_weight is None and q is not None and q_weight is not None:
+        dq_weight = _new(wide, torch.float32, like, stream)
+    if dk_weight is None and k is not None and k_weight is not None:
+        dk_weight = _new(wide, torch.float32, like, stream)
+    ws = None
+    if dq_weight is not None or dk_weight is not None:
+        ws = _workspace("pace_qk_norm_rotate_backward", size, workspace, like, stream)
+    with _On(like.device.index, stream) as s:
         _check("pace_qk_norm_rotate_backward", lib.pace_qk_norm_rotate_backward(
-            ctypes.byref(desc), _opt(q), _opt(k), *ptrs, _opt(grads[0]), _opt(grads[1]), _opt(outs[0]), _opt(outs[1]),
-            *dwp, _opt(ws), s))
-    return outs[0], outs[1], dws[0], dws[1]
+            ref, _opt(q), _opt(k), _opt(q_weight), _opt(k_weight), _opt(positions), _opt(inv_freq), _opt(d_q_out),
+            _opt(d_k_out), _opt(dq), _opt(dk), _opt(dq_weight), _opt(dk_weight), _opt(ws), s))
+    return dq, dk, dq_weight, dk_weight
 
 
 def pace_status_string(status: int) -> str:

@@ -11,25 +11,22 @@
 // on the 128 TMEM lanes:
 //   SC  [i, j]  = Q K^T                        (lanes i)
 //   OI  [e, i]  = bf16(S) Q^T                  A in TMEM
-//   OP  [e, i]  = V^T P,  P = bf16(mask A^|i-j| SC)   A in TMEM, P in shared memory
+//   OP  [e, i]  = V^T P,  P = mask A^|i-j| SC  V read MN-major, P in two bf16 parts
 //   U   [e, c]  = (V A^..)^T K                 A in TMEM in three bf16 parts, K read MN-major
 // out^T = OP + A^.. OI, and S stays in registers in fp32.
 //
-// Roundings: P and the copy of S that multiplies the query are bf16, once for
-// each term (2^-9 of it, the size of the output's own rounding).  The value
-// times its decay is split into three bf16 parts (24 bits), so that the
-// states, which are fp32 outputs and run over the whole sequence, are summed
-// from exact products of 24 bits; two parts left 2.7e-6 of the state.
+// Roundings: the copy of S that multiplies the query is bf16 (2^-9 of each term, the size of the output's own
+// rounding).  P is split into two bf16 parts (16 bits): rounded to one, short prompts came 1.5 times as far from the
+// exact outputs as those rounded once.  The value times its decay is split into three (24 bits), so that the states,
+// which are fp32 outputs and run over the whole sequence, are summed from exact products of 24 bits; two parts would
+// leave about 2e-6 of the state.
 //
-// One persistent CTA of 16 warps per SM:
-//  * warp 0: loads the chunks' tiles by TMA, three chunks ahead;
-//  * warp 1: issues the products.  SC of the next chunk goes before OP and U of
-//    this one, so that P is made while U runs;
-//  * warps 4-7: P from SC, then the value's raw and decayed parts into TMEM;
-//  * warps 8-15: the state (half of the key channels each four) and the output
-//    (half of the tokens each four).
-// Traffic is each input once and each output once; 128 d + 10 d^2 / ... products
-// a token keep the tensor pipe about half busy, so memory bounds it.
+// One persistent CTA of 28 warps per SM, each group of four (a TMEM lane quadrant each) with one job, so that their
+// latencies overlap:
+//  * warp 0: loads the chunks' tiles by TMA, three chunks ahead; warp 1: issues the products;
+//  * warps 4-11: the value's decayed parts into TMEM, half of the tokens each four;
+//  * warps 12-15: P from SC;  warps 16-19: the output, stored by TMA;
+//  * warps 20-27: the state, half of the key channels each four.
 //
 // Sequences too few to fill the SMs are cut into stretches: the same kernel
 // without outputs gives each stretch's own contribution to the state, a small
@@ -65,7 +62,7 @@ template <int D>
 struct alignas(1024) LinSmem {
   static constexpr int TILE = C * D * 2;                 // D / 64 blocks of 64 rows of 128 bytes
   uint8_t stage[NST][3][TILE];                           // query | key | value
-  uint8_t p[C * 128];                                    // P[i][j], 128-byte swizzle
+  uint8_t p[2][C * 128];                                 // P[i][j] in two bf16 parts, 128-byte swizzle
   uint8_t o[2][TILE];                                    // output tiles on their way to memory: 64 rows of 32 channels a warp
   // tables of the decay, of two items in turn, each group of warps its own:
   float wv[2][2][2][C];                                  // warps 4-7, 8-11: decay of a token's value in the state behind a
@@ -227,8 +224,8 @@ __device__ void mma_role(const LinTc& t, LinSmem<D>& sm) {
           for (int ks = 0; ks < 4; ++ks)
             ltc::mma_ts(T_OI, T_S + 32u * b + 8u * ks, q0 + (kStage * s + b * (C * 8) + ks * 2u), id_oi, b + ks > 0);
 #pragma unroll
-        for (int ks = 0; ks < C / 16; ++ks)
-          tc::mma_f16(T_OP, vt0 + (kStage * s + 128u * ks), p0 + 2u * ks, id_op, ks > 0);
+        for (int ks = 0; ks < 2 * (C / 16); ++ks)          // the parts of P one behind the other
+          tc::mma_f16(T_OP, vt0 + (kStage * s + 128u * (ks & 3)), p0 + (ks >> 2) * (C * 8) + 2u * (ks & 3), id_op, ks > 0);
         tc::commit(&sm.op_full);
         tc::commit(&sm.empty[s]);
       }
@@ -257,9 +254,13 @@ __device__ __forceinline__ void make_p(uint32_t p_smem, const float* pz, int sgn
   const float* at = pz + sgn * (16 * qd + g - 2 * q + 8);
   const uint32_t row = 16 * qd + (lane & 15);    // stmatrix: the row whose address this lane gives
   float2 w0 = make_float2(at[0], at[-sgn]);
+  auto split = [](float2 x, uint32_t* hi, uint32_t* lo) {
+    *hi = ltc::pack_bf16(x.x, x.y);
+    *lo = ltc::pack_bf16(x.x - ltc::bf16_lo(*hi), x.y - ltc::bf16_hi(*hi));
+  };
 #pragma unroll 1
   for (int c = 0; c < 8; c += 2) {
-    uint32_t sc[8], m[4];
+    uint32_t sc[8], m[4], l[4];
     ltc::ld_16x256b_x2(((uint32_t)(32 * qd) << 16) + T_SC + 8 * c, sc);
     const float2 w1 = make_float2(at[-8 * sgn], at[-9 * sgn]), w2 = make_float2(at[-16 * sgn], at[-17 * sgn]);
     at -= 16 * sgn;
@@ -275,12 +276,14 @@ __device__ __forceinline__ void make_p(uint32_t p_smem, const float* pz, int sgn
       const int x = 4 * y;
       const float2 a = __fmul2_rn(make_float2(__uint_as_float(sc[x]), __uint_as_float(sc[x + 1])), w[y + 1]);
       const float2 b = __fmul2_rn(make_float2(__uint_as_float(sc[x + 2]), __uint_as_float(sc[x + 3])), w[y]);
-      m[2 * y] = ltc::pack_bf16(a.x, a.y);
-      m[2 * y + 1] = ltc::pack_bf16(b.x, b.y);
+      split(a, &m[2 * y], &l[2 * y]);
+      split(b, &m[2 * y + 1], &l[2 * y + 1]);
     }
     w0 = w2;
     // matrices: (rows 0-7, block c), (rows 8-15, block c), (rows 0-7, block c + 1), (rows 8-15, block c + 1)
-    ltc::stsm_x4(p_smem + row * 128 + (((c + (lane >> 4)) ^ (row & 7)) << 4), m[0], m[1], m[2], m[3]);
+    const uint32_t to = p_smem + row * 128 + (((c + (lane >> 4)) ^ (row & 7)) << 4);
+    ltc::stsm_x4(to, m[0], m[1], m[2], m[3]);
+    ltc::stsm_x4(to + C * 128, l[0], l[1], l[2], l[3]);
   }
 }
 

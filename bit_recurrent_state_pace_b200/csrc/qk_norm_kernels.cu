@@ -4,14 +4,12 @@
 //   y = s R(pos) (w * x r),  r = (sum x^2 / n + eps)^(-1/2)
 //   u = s R(-pos) dy,  dw = sum u * x^,  h = u * w,  dx = r (h - x^ (x^ . h) / n),  x^ = x r
 //
-// Memory-bound: 2 (3 in the backward pass) times the tensors' bytes.  The rows
-// of all tokens, each token's queries before its keys, are one list; a block
-// of 256 threads takes a stretch of it.  A row is held by L lanes of one warp,
-// 8 elements (one 16-byte load in bf16) each, so a warp's loads are full lines
-// and both sums are shuffles; a thread has U rows' loads in flight.  Angles
-// are computed once for each token of the stretch, into shared memory, while
-// the loads fly: pos * inv_freq / 2 pi in fp64, whose fraction alone goes on
-// in fp32, so that far positions lose nothing.
+// Memory-bound: 2 (3 in the backward pass) times the tensors' bytes.  A row (one head of one token) is held by L lanes
+// of one warp, 8 elements (one 16-byte load in bf16) each, so a warp's loads are full lines and both sums are shuffles.
+// A block walks over tiles -- some tokens with all their heads, or a part of one token's -- with the next tile's loads
+// in flight and its tokens' angles being computed while it works on one: a thread keeps its columns, so the weights stay
+// in registers.  The angle pos * inv_freq / 2 pi is taken in fp64 and only its fraction goes on in fp32: far positions
+// lose nothing, and each token's angles are computed once for all its heads.
 #include "linattn.cuh"
 
 namespace pace {
@@ -20,7 +18,8 @@ namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kMaxBackBlocks = 148 * 4;
+constexpr int kSms = 148;                  // B200
+constexpr int kBlocks = kSms * 2;          // resident: two of 256 threads an SM
 
 // lanes that hold a row: the power of two that gives each at most 8 elements
 inline int lanes_of(int D) {
@@ -29,63 +28,84 @@ inline int lanes_of(int D) {
   return L;
 }
 
-struct Row {
-  bool in;          // there is such a row and this lane holds a part of it
-  int side, head, ltok;
-  size_t tok;
+// How the rows are cut into tiles.
+struct NormTiles {
+  int32_t L, R;             // lanes a row, rows a token
+  uint32_t magic;           // ceil(2^32 / R): x / R = umulhi(x, magic) for x < 2^16 (R > 1)
+  int32_t tokens, passes;   // tokens a tile; tiles that share them
+  int64_t tiles;
+};
+
+// One row's eight elements of this lane, as they lie in memory.
+template <bool BF16>
+struct Raw {
+  uint32_t w[BF16 ? 4 : 8];
 };
 
 template <bool BF16, bool VEC>
-__device__ __forceinline__ void load8(const void* p, size_t at, float (&x)[8]) {
-  if (BF16) {
-    if (VEC) {
-      const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + at);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = load_io(p, at + j, PACE_IO_BF16);
+__device__ __forceinline__ Raw<BF16> load_raw(const void* p, size_t at) {
+  Raw<BF16> r;
+  if (VEC) {
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) + at * (BF16 ? 2 : 4));
+    const uint4 a = q[0];
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+    if (!BF16) {
+      const uint4 b = q[1];
+      r.w[BF16 ? 0 : 4] = b.x, r.w[BF16 ? 1 : 5] = b.y, r.w[BF16 ? 2 : 6] = b.z, r.w[BF16 ? 3 : 7] = b.w;
     }
+  } else if (BF16) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + at;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = (uint32_t)q[2 * j] | ((uint32_t)q[2 * j + 1] << 16);
   } else {
-    const float* f = reinterpret_cast<const float*>(p) + at;
-    if (VEC) {
-      const float4 a = *reinterpret_cast<const float4*>(f), b = *reinterpret_cast<const float4*>(f + 4);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + at;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = f[j];
-    }
+    for (int j = 0; j < (BF16 ? 4 : 8); ++j) r.w[j] = q[j];
+  }
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> zero_raw() {
+  Raw<BF16> r;
+#pragma unroll
+  for (int j = 0; j < (BF16 ? 4 : 8); ++j) r.w[j] = 0u;
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(const Raw<BF16>& r, float2 (&x)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (BF16) x[j] = make_float2(__uint_as_float(r.w[j] << 16), __uint_as_float(r.w[j] & 0xffff0000u));
+    else x[j] = make_float2(__uint_as_float(r.w[BF16 ? 0 : 2 * j]), __uint_as_float(r.w[BF16 ? 0 : 2 * j + 1]));
   }
 }
 
 template <bool BF16, bool VEC>
-__device__ __forceinline__ void store8(void* p, size_t at, const float (&x)[8]) {
+__device__ __forceinline__ void store8(void* p, size_t at, const float2 (&x)[4]) {
   if (BF16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __float22bfloat162_rn(x[j]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
     uint16_t* b = reinterpret_cast<uint16_t*>(p) + at;
     if (VEC) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&h);
-      }
       *reinterpret_cast<uint4*>(b) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) b[j] = float_to_bf16_bits_rn(x[j]);
+      for (int j = 0; j < 8; ++j) b[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
     }
   } else {
     float* f = reinterpret_cast<float*>(p) + at;
     if (VEC) {
-      *reinterpret_cast<float4*>(f) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(f + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<float4*>(f) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+      *reinterpret_cast<float4*>(f + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = x[j];
+      for (int j = 0; j < 4; ++j) f[2 * j] = x[j].x, f[2 * j + 1] = x[j].y;
     }
   }
 }
@@ -94,218 +114,231 @@ __device__ __forceinline__ float row_sum(float s, int L) {
   for (int off = L >> 1; off; off >>= 1) s += __shfl_xor_sync(FULL, s, off);
   return s;
 }
+__device__ __forceinline__ float dot8(const float2 (&a)[4], const float2 (&b)[4]) {
+  float2 s = __fmul2_rn(a[0], b[0]);
+#pragma unroll
+  for (int j = 1; j < 4; ++j) s = __ffma2_rn(a[j], b[j], s);
+  return s.x + s.y;
+}
 
-// cos and sin of every pair's angle for the `ntok` tokens from tok0 on: tab[ltok][pair]
-__device__ __forceinline__ void angle_table(const NormArgs& a, float2* tab, size_t tok0, int ntok) {
+// How the rotation's pairs lie: in one lane (interleaved), half a row of whole lanes apart, or otherwise apart.
+enum Pairs { PAIRS_NONE, PAIRS_LANE, PAIRS_LANES, PAIRS_ANY };
+__host__ __device__ inline Pairs pairs_of(const NormArgs& a) {
+  if (!a.rot) return PAIRS_NONE;
+  if (a.interleaved) return a.rot % 8 == 0 ? PAIRS_LANE : PAIRS_ANY;
+  return a.rot % 16 == 0 ? PAIRS_LANES : PAIRS_ANY;
+}
+// Place of pair i in a token's table.  A lane reads its 4 or 8 pairs two at a time; a step's reads of all lanes lie side
+// by side.
+__device__ __forceinline__ int pair_place(Pairs p, int half, int i) {
+  if (p == PAIRS_LANE) return (((i & 3) >> 1) * (half >> 2) + (i >> 2)) * 2 + (i & 1);
+  if (p == PAIRS_LANES) return (((i & 7) >> 1) * (half >> 3) + (i >> 3)) * 2 + (i & 1);
+  return i;
+}
+
+// cos and sin of every pair's angle for `ntok` tokens from tok0 on: tab[token][place]
+__device__ __forceinline__ void angle_table(const NormArgs& a, Pairs p, float2* tab, int64_t tok0, int ntok) {
   const int half = a.rot >> 1;
   for (int e = threadIdx.x; e < ntok * half; e += kThreads) {
     const int lt = e / half, i = e - lt * half;
-    if (tok0 + lt < (size_t)a.tokens) {
+    float2 cs = make_float2(1.f, 0.f);               // behind the last token: rows of zeros, turned by nothing
+    if (tok0 + lt < a.tokens) {
       const double turns = (double)a.pos[tok0 + lt] * (double)a.inv_freq[i] * 0.15915494309189533577;
-      const float f = (float)(turns - rint(turns));
-      float s, c;
-      sincospif(2.f * f, &s, &c);
-      tab[e] = make_float2(c, s);
+      sincospif(2.f * (float)(turns - rint(turns)), &cs.y, &cs.x);
     }
+    tab[lt * half + pair_place(p, half, i)] = cs;
   }
 }
 
-// Turns the row held by the lanes of this group by `sgn` times its angles.  c: the lane's place in its row.
-// Half-split pairs lie rotary_dim / 2 apart: whole lanes apart where that is a multiple of 8, and come by
-// shuffles; else through shared memory.
-__device__ __forceinline__ void turn8(const NormArgs& a, float (&y)[8], const float2* t, float sgn, int c, int L, float* xch) {
+// Turns the row held by the lanes of this group by `sgn` times its angles.  c: the lane's place in its row; xch: shared
+// memory of 8 floats a thread, for pairs that lie anyhow.
+__device__ __forceinline__ void turn8(const NormArgs& a, Pairs p, float2 (&y)[4], const float2* t, float sgn, int c, float* xch) {
   const int col = 8 * c, half = a.rot >> 1;
-  if (a.interleaved) {
+  if (p == PAIRS_LANE) {
     if (col < a.rot) {
+      const float4* t4 = reinterpret_cast<const float4*>(t) + c;
+      const int step = half >> 2;
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        if (col + j < a.rot) {
-          const float2 cs = t[(col + j) >> 1];
-          const float s = sgn * cs.y, u = y[j], v = y[j + 1];
-          y[j] = u * cs.x - v * s;
-          y[j + 1] = v * cs.x + u * s;
-        }
+      for (int j = 0; j < 4; j += 2) {
+        const float4 cs = t4[(j >> 1) * step];
+        const float s0 = sgn * cs.y, s1 = sgn * cs.w;
+        y[j] = make_float2(y[j].x * cs.x - y[j].y * s0, y[j].y * cs.x + y[j].x * s0);
+        y[j + 1] = make_float2(y[j + 1].x * cs.z - y[j + 1].y * s1, y[j + 1].y * cs.z + y[j + 1].x * s1);
       }
     }
-    return;
-  }
-  if ((half & 7) == 0) {
+  } else if (p == PAIRS_LANES) {
     const int lane = threadIdx.x & 31, hl = half >> 3, base = lane - c;
-    const int from = c < hl ? c + hl : (c < 2 * hl ? c - hl : c);
-    const float flip = c < hl ? -sgn : sgn;
-    const bool on = c < 2 * hl;
-    const int i0 = c < hl ? col : col - half;
+    const bool low = c < hl, on = c < 2 * hl;
+    const int mate = low ? c + hl : (on ? c - hl : c);
+    const float flip = low ? -sgn : sgn;
+    const float4* t4 = reinterpret_cast<const float4*>(t) + (low ? c : (on ? c - hl : 0));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float ox = __shfl_sync(FULL, y[j].x, base + mate), oy = __shfl_sync(FULL, y[j].y, base + mate);
+      const float4 cs = t4[j * hl];
+      if (on) y[j] = make_float2(y[j].x * cs.x + ox * (flip * cs.y), y[j].y * cs.z + oy * (flip * cs.w));
+    }
+  } else {
+    float* mine = xch + (size_t)(threadIdx.x - c) * 8;    // the row, 8 L floats
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine[col + 2 * j] = y[j].x, mine[col + 2 * j + 1] = y[j].y;
+    __syncwarp();
+    float z[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float o = __shfl_sync(FULL, y[j], base + from);
-      if (on) {
-        const float2 cs = t[i0 + j];
-        y[j] = y[j] * cs.x + o * (flip * cs.y);
+      const int x = col + j;
+      z[j] = mine[col + j];
+      if (x < a.rot) {
+        const int i = a.interleaved ? x >> 1 : (x < half ? x : x - half);
+        const bool first = a.interleaved ? !(x & 1) : x < half;
+        const float other = mine[a.interleaved ? x ^ 1 : (first ? x + half : x - half)];
+        const float2 cs = t[i];
+        z[j] = z[j] * cs.x + other * ((first ? -sgn : sgn) * cs.y);
       }
     }
-    return;
-  }
-  float* mine = xch + (size_t)(threadIdx.x - c) * 8;    // the row, 8 L floats
+    __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) mine[col + j] = y[j];
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int x = col + j;
-    if (x < half) {
-      const float2 cs = t[x];
-      y[j] = y[j] * cs.x - mine[x + half] * (sgn * cs.y);
-    } else if (x < a.rot) {
-      const float2 cs = t[x - half];
-      y[j] = y[j] * cs.x + mine[x - half] * (sgn * cs.y);
-    }
+    for (int j = 0; j < 4; ++j) y[j] = make_float2(z[2 * j], z[2 * j + 1]);
   }
-  __syncwarp();
 }
 
-// Row `first + off` of the list, first being row r0 of token tok0.
-__device__ __forceinline__ Row locate(const NormArgs& a, int64_t first, int64_t rows, size_t tok0, int r0, int R, int off, int c) {
+// Where row x of a tile lies.
+struct Row {
+  bool in;                  // there is such a row and this lane holds a part of it
+  int side, head, ltok;
+  int64_t tok;
+};
+__device__ __forceinline__ Row locate(const NormArgs& a, const NormTiles& n, int64_t tok0, int x, int c) {
   Row r;
-  const int x = r0 + off;
-  r.ltok = x / R;
-  int head = x - r.ltok * R;
-  r.side = head >= a.side[0].heads ? 1 : 0;
-  r.head = r.side ? head - a.side[0].heads : head;
+  r.ltok = n.R > 1 ? (int)__umulhi((uint32_t)x, n.magic) : x;
+  const int row = x - r.ltok * n.R;
+  r.side = row >= a.side[0].heads;
+  r.head = r.side ? row - a.side[0].heads : row;
   r.tok = tok0 + r.ltok;
-  r.in = first + off < rows && 8 * c < a.D;
+  r.in = r.ltok < n.tokens && r.tok < a.tokens && 8 * c < a.D;
+  if (r.ltok >= n.tokens) r.ltok = n.tokens - 1;
   return r;
 }
 
-template <bool BF16, bool VEC, int U>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const __grid_constant__ NormArgs a, int L) {
-  extern __shared__ float2 tab[];
-  float* xch = nullptr;
-  const int c = threadIdx.x & (L - 1), slot = threadIdx.x / L, slots = kThreads / L;
-  const int R = a.side[0].heads + a.side[1].heads;
-  const int64_t rows = (int64_t)a.tokens * R, first = (int64_t)blockIdx.x * (slots * U);
-  const size_t tok0 = (size_t)(first / R);
-  const int r0 = (int)(first - (int64_t)tok0 * R);
-  Row row[U];
-  float x[U][8];
+// BACK 0: the operator; 1: its gradient; 2: with the weights' gradients.  U rows a thread and tile.
+template <bool BF16, bool VEC, int U, int BACK>
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ NormTiles n) {
+  extern __shared__ __align__(16) float2 shared[];
+  const Pairs pairs = pairs_of(a);
+  const int L = n.L, c = threadIdx.x & (L - 1), slots = kThreads / L, slot = threadIdx.x / L;
+  const int tab_size = n.tokens * (a.rot >> 1) + ((n.tokens * (a.rot >> 1)) & 1);
+  float2* tab[2] = {shared, shared + tab_size};
+  float* xch = reinterpret_cast<float*>(shared + 2 * tab_size);
+  float2 w[2][4];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    row[u] = locate(a, first, rows, tok0, r0, R, u * slots + slot, c);
-    const NormSide& s = a.side[row[u].side];
-    if (row[u].in) load8<BF16, VEC>(s.x, row[u].tok * s.x_stride + (size_t)row[u].head * a.D + 8 * c, x[u]);
-    else {
+  for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[u][j] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      w[s][j] = make_float2(1.f, 1.f);
+      if (a.side[s].w && 8 * c < a.D) w[s][j] = make_float2(a.side[s].w[8 * c + 2 * j], a.side[s].w[8 * c + 2 * j + 1]);
     }
+  float2 dw[2][4];
+  if (BACK == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[0][j] = dw[1][j] = make_float2(0.f, 0.f);
   }
-  if (a.rot) {
-    const int ntok = (r0 + slots * U - 1) / R + 1;
-    angle_table(a, tab, tok0, ntok);
-    xch = reinterpret_cast<float*>(tab + (size_t)ntok * (a.rot >> 1));
+  auto first_token = [&](int64_t tile, int* x0) {
+    const int64_t group = n.passes > 1 ? tile / n.passes : tile;
+    *x0 = (int)(tile - group * n.passes) * (slots * U) + slot;
+    return group * n.tokens;
+  };
+  Raw<BF16> nx[U], ng[BACK ? U : 1];
+  auto fetch = [&](int64_t tile) {
+    int x0;
+    const int64_t tok0 = first_token(tile, &x0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Row r = locate(a, n, tok0, x0 + u * slots, c);
+      const NormSide& s = a.side[r.side];
+      nx[u] = zero_raw<BF16>();
+      if (BACK) ng[BACK ? u : 0] = zero_raw<BF16>();
+      if (r.in) {
+        nx[u] = load_raw<BF16, VEC>(s.x, (size_t)(r.tok * s.x_stride) + (size_t)r.head * a.D + 8 * c);
+        if (BACK) ng[BACK ? u : 0] = load_raw<BF16, VEC>(s.dy, (size_t)(r.tok * s.heads + r.head) * a.D + 8 * c);
+      }
+    }
+    return tok0;
+  };
+  int64_t tile = blockIdx.x;
+  int64_t tok0 = fetch(tile);
+  int cur = 0;
+  if (pairs != PAIRS_NONE) {
+    angle_table(a, pairs, tab[0], tok0, n.tokens);
     __syncthreads();
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const NormSide& s = a.side[row[u].side];
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[u][j], x[u][j], ss);
-    ss = row_sum(ss, L);
-    const float r = rsqrtf(fmaf(ss, a.inv_n, a.eps));
-    if (s.w && row[u].in) {
-      float w[8];
-      load8<false, false>(s.w, 8 * c, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[u][j] = x[u][j] * r * w[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[u][j] *= r;
-    }
-    if (a.rot) turn8(a, x[u], tab + (size_t)row[u].ltok * (a.rot >> 1), 1.f, c, L, xch);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[u][j] *= s.scale;
-    if (row[u].in) store8<BF16, VEC>(s.y, row[u].tok * s.y_stride + (size_t)row[u].head * a.D + 8 * c, x[u]);
-  }
-}
-
-template <bool BF16, bool VEC, int U, bool DW>
-__global__ void __launch_bounds__(kThreads) qk_norm_backward_kernel(const __grid_constant__ NormArgs a, int L, int64_t tiles) {
-  extern __shared__ float2 tab[];
-  const int c = threadIdx.x & (L - 1), slot = threadIdx.x / L, slots = kThreads / L;
-  const int R = a.side[0].heads + a.side[1].heads;
-  const int64_t rows = (int64_t)a.tokens * R;
-  const int maxtok = a.rot ? (R - 1 + slots * U - 1) / R + 1 : 0;
-  float* xch = reinterpret_cast<float*>(tab + (size_t)maxtok * (a.rot >> 1));
-  float dw[2][8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t first = tile * (slots * U);
-    const size_t tok0 = (size_t)(first / R);
-    const int r0 = (int)(first - (int64_t)tok0 * R);
-    Row row[U];
-    float x[U][8], g[U][8];
+  for (; tile < n.tiles; tile += gridDim.x, cur ^= 1) {
+    Raw<BF16> rx[U], rg[BACK ? U : 1];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      row[u] = locate(a, first, rows, tok0, r0, R, u * slots + slot, c);
-      const NormSide& s = a.side[row[u].side];
-      if (row[u].in) {
-        load8<BF16, VEC>(s.x, row[u].tok * s.x_stride + (size_t)row[u].head * a.D + 8 * c, x[u]);
-        load8<BF16, VEC>(s.dy, (row[u].tok * s.heads + row[u].head) * a.D + 8 * c, g[u]);
+      rx[u] = nx[u];
+      if (BACK) rg[BACK ? u : 0] = ng[BACK ? u : 0];
+    }
+    int x0;
+    tok0 = first_token(tile, &x0);
+    const bool more = tile + gridDim.x < n.tiles;
+    if (more) {
+      const int64_t next = fetch(tile + gridDim.x);
+      if (pairs != PAIRS_NONE) angle_table(a, pairs, tab[cur ^ 1], next, n.tokens);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Row r = locate(a, n, tok0, x0 + u * slots, c);
+      const NormSide& s = a.side[r.side];
+      const float2* t = tab[cur] + r.ltok * (a.rot >> 1);
+      const size_t at = (size_t)(r.tok * s.y_stride) + (size_t)r.head * a.D + 8 * c;
+      float2 x[4], ww[4];
+      unpack<BF16>(rx[u], x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ww[j] = r.side ? w[1][j] : w[0][j];
+      const float rr = rsqrtf(fmaf(row_sum(dot8(x, x), L), a.inv_n, a.eps));
+      if (!BACK) {
+        const float2 f = make_float2(rr * s.scale, rr * s.scale);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(__fmul2_rn(x[j], f), ww[j]);
+        if (pairs != PAIRS_NONE) turn8(a, pairs, x, t, 1.f, c, xch);
+        if (r.in) store8<BF16, VEC>(s.y, at, x);
       } else {
+        float2 g[4];
+        unpack<BF16>(rg[BACK ? u : 0], g);
+        if (pairs != PAIRS_NONE) turn8(a, pairs, g, t, -1.f, c, xch);
+        const float2 r2 = make_float2(rr, rr), sc = make_float2(s.scale, s.scale);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[u][j] = g[u][j] = 0.f;
-      }
-    }
-    if (a.rot) {
-      if (tile != (int64_t)blockIdx.x) __syncthreads();      // the last tile's table is done with
-      angle_table(a, tab, tok0, (r0 + slots * U - 1) / R + 1);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const NormSide& s = a.side[row[u].side];
-      if (a.rot) turn8(a, g[u], tab + (size_t)row[u].ltok * (a.rot >> 1), -1.f, c, L, xch);
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[u][j], x[u][j], ss);
-      ss = row_sum(ss, L);
-      const float r = rsqrtf(fmaf(ss, a.inv_n, a.eps));
-      float w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = 1.f;
-      if (s.w && row[u].in) load8<false, false>(s.w, 8 * c, w);
-      float dot = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[u][j] *= r;                                         // x^
-        g[u][j] *= s.scale;                                   // u
-        if (DW) {
-          const float t = x[u][j] * g[u][j];
-          if (row[u].in) {
-            if (row[u].side) dw[1][j] += t;
-            else dw[0][j] += t;
+        for (int j = 0; j < 4; ++j) {
+          x[j] = __fmul2_rn(x[j], r2);                          // x^
+          g[j] = __fmul2_rn(g[j], sc);                          // u
+          if (BACK == 2) {
+            const float2 z = make_float2(0.f, 0.f);
+            const float2 keep = r.in ? x[j] : z;
+            dw[0][j] = __ffma2_rn(r.side ? z : keep, g[j], dw[0][j]);
+            dw[1][j] = __ffma2_rn(r.side ? keep : z, g[j], dw[1][j]);
           }
+          g[j] = __fmul2_rn(g[j], ww[j]);                       // h
         }
-        g[u][j] *= w[j];                                      // h
-        dot = fmaf(x[u][j], g[u][j], dot);
-      }
-      dot = row_sum(dot, L) * a.inv_n;
+        const float d = row_sum(dot8(x, g), L) * -a.inv_n;
+        const float2 d2 = make_float2(d, d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[u][j] = r * (g[u][j] - x[u][j] * dot);
-      if (row[u].in) store8<BF16, VEC>(s.y, row[u].tok * s.y_stride + (size_t)row[u].head * a.D + 8 * c, g[u]);
+        for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(r2, __ffma2_rn(x[j], d2, g[j]));
+        if (r.in) store8<BF16, VEC>(s.y, at, g);
+      }
     }
+    if (pairs != PAIRS_NONE && more) __syncthreads();           // the next table is whole, this one is done with
   }
-  if (DW) {
-    // this block's sums: over its row slots, in the order of the slots
-    __shared__ float red[kThreads * 8];
+  if (BACK == 2) {
+    // this block's sums over its row slots, in the order of the slots
+    __shared__ float2 red[kThreads * 4];
     for (int side = 0; side < 2; ++side) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) red[threadIdx.x * 8 + j] = dw[side][j];
+      for (int j = 0; j < 4; ++j) red[threadIdx.x * 4 + j] = dw[side][j];
       __syncthreads();
       for (int col = threadIdx.x; col < a.D; col += kThreads) {
         float s = 0.f;
-        for (int k = 0; k < slots; ++k) s += red[k * L * 8 + col];
+        for (int k = 0; k < slots; ++k) s += reinterpret_cast<const float*>(red)[k * L * 8 + col];
         a.partial[((size_t)blockIdx.x * 2 + side) * a.D + col] = s;
       }
     }
@@ -342,57 +375,61 @@ bool aligned16(const NormArgs& a, bool back) {
   return true;
 }
 
-// tokens that a stretch of `rows` rows can touch
-size_t table_bytes(const NormArgs& a, int rows, bool exchange) {
-  const int R = a.side[0].heads + a.side[1].heads;
-  const size_t ntok = a.rot ? (size_t)(R - 1 + rows - 1) / R + 1 : 0;
-  return ntok * (a.rot / 2) * sizeof(float2) + (exchange ? kThreads * 8 * sizeof(float) : 0);
+// Tiles of `per` rows: as many whole tokens as fit, or a part of one.
+NormTiles tiles_of(const NormArgs& a, int per) {
+  NormTiles n;
+  n.L = lanes_of(a.D);
+  n.R = a.side[0].heads + a.side[1].heads;
+  n.magic = n.R > 1 ? (uint32_t)((((uint64_t)1 << 32) + n.R - 1) / n.R) : 0;
+  n.tokens = per >= n.R ? per / n.R : 1;
+  n.passes = per >= n.R ? 1 : (n.R + per - 1) / per;
+  n.tiles = ((int64_t)a.tokens + n.tokens - 1) / n.tokens * n.passes;
+  return n;
 }
 
-inline bool needs_exchange(const NormArgs& a) { return a.rot && !a.interleaved && (a.rot / 2) % 8 != 0; }
+size_t shared_bytes(const NormArgs& a, const NormTiles& n) {
+  const size_t t = (size_t)n.tokens * (a.rot / 2);
+  return 2 * (t + (t & 1)) * sizeof(float2) + (pairs_of(a) == PAIRS_ANY ? kThreads * 8 * sizeof(float) : 0);
+}
 
-template <bool BF16, bool VEC, int U>
-cudaError_t forward(const NormArgs& a, int64_t rows, int L, cudaStream_t st) {
-  const int per = kThreads / L * U;
-  const int64_t blocks = (rows + per - 1) / per;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  qk_norm_kernel<BF16, VEC, U><<<(unsigned)blocks, kThreads, table_bytes(a, per, needs_exchange(a)), st>>>(a, L);
+template <bool BF16, bool VEC, int U, int BACK>
+cudaError_t launch_u(const NormArgs& a, cudaStream_t st, int* blocks_out) {
+  const NormTiles n = tiles_of(a, kThreads / lanes_of(a.D) * U);
+  const size_t smem = shared_bytes(a, n);
+  const int64_t most = kBlocks;
+  const int blocks = (int)(n.tiles < most ? n.tiles : most);
+  if (blocks_out) *blocks_out = blocks;
+  if (smem > 48 * 1024) {          // small heads in fp32 rows of one token each: tables of 32 KB and more
+    const cudaError_t e = cudaFuncSetAttribute(qk_norm_kernel<BF16, VEC, U, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  qk_norm_kernel<BF16, VEC, U, BACK><<<blocks, kThreads, smem, st>>>(a, n);
   return cudaGetLastError();
 }
 
-template <bool BF16, bool VEC>
-cudaError_t backward(const NormArgs& a, int64_t rows, int L, cudaStream_t st) {
-  constexpr int U = 2;
-  const int per = kThreads / L * U;
-  const int64_t tiles = (rows + per - 1) / per;
-  const int blocks = (int)(tiles < kMaxBackBlocks ? tiles : kMaxBackBlocks);
-  const size_t smem = table_bytes(a, per, needs_exchange(a));
-  const bool dw = a.side[0].dw || a.side[1].dw;
-  if (dw) qk_norm_backward_kernel<BF16, VEC, U, true><<<blocks, kThreads, smem, st>>>(a, L, tiles);
-  else qk_norm_backward_kernel<BF16, VEC, U, false><<<blocks, kThreads, smem, st>>>(a, L, tiles);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !dw) return e;
-  qk_norm_reduce_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, st>>>(a.partial, blocks, a.D, a.side[0].dw, a.side[1].dw);
-  return cudaGetLastError();
+// U rows a thread where that still gives every SM some blocks, else one.
+template <bool BF16, bool VEC, int BACK>
+cudaError_t launch_t(const NormArgs& a, int64_t rows, cudaStream_t st, int* blocks) {
+  constexpr int U = BACK ? (BF16 ? 2 : 1) : (BF16 ? 4 : 2);
+  if (U == 1 || rows * lanes_of(a.D) / (kThreads * U) < 2 * kSms) return launch_u<BF16, VEC, 1, BACK>(a, st, blocks);
+  return launch_u<BF16, VEC, U, BACK>(a, st, blocks);
+}
+
+template <int BACK>
+cudaError_t launch(const NormArgs& a, int64_t rows, cudaStream_t st, int* blocks) {
+  const bool vec = aligned16(a, BACK != 0);
+  if (a.io == PACE_IO_BF16)
+    return vec ? launch_t<true, true, BACK>(a, rows, st, blocks) : launch_t<true, false, BACK>(a, rows, st, blocks);
+  return vec ? launch_t<false, true, BACK>(a, rows, st, blocks) : launch_t<false, false, BACK>(a, rows, st, blocks);
 }
 
 }  // namespace
 
-size_t qk_norm_partial_bytes(int64_t, int D) { return (size_t)kMaxBackBlocks * 2 * D * sizeof(float); }
+size_t qk_norm_partial_bytes(int64_t, int D) { return (size_t)kBlocks * 2 * D * sizeof(float); }
 
 cudaError_t launch_qk_norm(const NormArgs& a, cudaStream_t st) {
   const int64_t rows = (int64_t)a.tokens * (a.side[0].heads + a.side[1].heads);
-  if (rows == 0) return cudaSuccess;
-  const int L = lanes_of(a.D);
-  const bool vec = aligned16(a, false), bf = a.io == PACE_IO_BF16;
-  // few rows: one a thread, so that they spread over the SMs
-  const bool few = rows * L / kThreads < 148 * 8;
-  if (few) {
-    if (bf) return vec ? forward<true, true, 1>(a, rows, L, st) : forward<true, false, 1>(a, rows, L, st);
-    return vec ? forward<false, true, 1>(a, rows, L, st) : forward<false, false, 1>(a, rows, L, st);
-  }
-  if (bf) return vec ? forward<true, true, 4>(a, rows, L, st) : forward<true, false, 4>(a, rows, L, st);
-  return vec ? forward<false, true, 4>(a, rows, L, st) : forward<false, false, 4>(a, rows, L, st);
+  return rows == 0 ? cudaSuccess : launch<0>(a, rows, st, nullptr);
 }
 
 cudaError_t launch_qk_norm_backward(const NormArgs& a, cudaStream_t st) {
@@ -405,10 +442,12 @@ cudaError_t launch_qk_norm_backward(const NormArgs& a, cudaStream_t st) {
     }
     return cudaSuccess;
   }
-  const int L = lanes_of(a.D);
-  const bool vec = aligned16(a, true), bf = a.io == PACE_IO_BF16;
-  if (bf) return vec ? backward<true, true>(a, rows, L, st) : backward<true, false>(a, rows, L, st);
-  return vec ? backward<false, true>(a, rows, L, st) : backward<false, false>(a, rows, L, st);
+  if (!a.side[0].dw && !a.side[1].dw) return launch<1>(a, rows, st, nullptr);
+  int blocks = 0;
+  const cudaError_t e = launch<2>(a, rows, st, &blocks);
+  if (e != cudaSuccess) return e;
+  qk_norm_reduce_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, st>>>(a.partial, blocks, a.D, a.side[0].dw, a.side[1].dw);
+  return cudaGetLastError();
 }
 
 }  // namespace pace
