@@ -4,12 +4,15 @@
 //   y = s R(pos) (w * x r),  r = (sum x^2 / n + eps)^(-1/2)
 //   u = s R(-pos) dy,  dw = sum u * x^,  h = u * w,  dx = r (h - x^ (x^ . h) / n),  x^ = x r
 //
-// Memory-bound: 2 (3 in the backward pass) times the tensors' bytes.  A row (one head of one token) is held by L lanes
-// of one warp, 8 elements (one 16-byte load in bf16) each, so a warp's loads are full lines and both sums are shuffles.
-// A block walks over tiles -- some tokens with all their heads, or a part of one token's -- with the next tile's loads
-// in flight and its tokens' angles being computed while it works on one: a thread keeps its columns, so the weights stay
-// in registers.  The angle pos * inv_freq / 2 pi is taken in fp64 and only its fraction goes on in fp32: far positions
-// lose nothing, and each token's angles are computed once for all its heads.
+// Memory-bound: 2 (3 in the backward pass) times the tensors' bytes, so what counts beside enough loads in flight is the
+// number of instructions a row.  A row (one head of one token) is held by L lanes of a warp, 8 elements (one 16-byte load
+// in bf16) each, so a warp's loads are full lines and both sums are shuffles.  A warp takes a token (or, where there are
+// few, a part of one) and goes through its queries, then its keys, U rows a lane at a time with the next ones' loads in
+// flight: a lane keeps its columns, so the weights, and the token's cosines and sines, stay in registers.  The angle
+// pos * inv_freq / 2 pi is taken in fp64 and only its fraction goes on in fp32: far positions lose nothing.
+//
+// Blocks with one table of angles for their tokens, rows in a flat list, took 174 instructions a row (this: about 80) and
+// waited at a barrier for the table.
 #include "linattn.cuh"
 
 namespace pace {
@@ -17,9 +20,10 @@ namespace pace {
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSms = 148;                  // B200
-constexpr int kBlocks = kSms * 2;          // resident: two of 256 threads an SM
+constexpr int kBlocks = kSms * 2;          // resident: two an SM
+constexpr int kMaxD = 256;
 
 // lanes that hold a row: the power of two that gives each at most 8 elements
 inline int lanes_of(int D) {
@@ -28,14 +32,6 @@ inline int lanes_of(int D) {
   return L;
 }
 
-// How the rows are cut into tiles.
-struct NormTiles {
-  int32_t L, R;             // lanes a row, rows a token
-  uint32_t magic;           // ceil(2^32 / R): x / R = umulhi(x, magic) for x < 2^16 (R > 1)
-  int32_t tokens, passes;   // tokens a tile; tiles that share them
-  int64_t tiles;
-};
-
 // One row's eight elements of this lane, as they lie in memory.
 template <bool BF16>
 struct Raw {
@@ -43,10 +39,10 @@ struct Raw {
 };
 
 template <bool BF16, bool VEC>
-__device__ __forceinline__ Raw<BF16> load_raw(const void* p, size_t at) {
+__device__ __forceinline__ Raw<BF16> load_raw(const uint8_t* p) {
   Raw<BF16> r;
   if (VEC) {
-    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) + at * (BF16 ? 2 : 4));
+    const uint4* q = reinterpret_cast<const uint4*>(p);
     const uint4 a = q[0];
     r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
     if (!BF16) {
@@ -54,11 +50,11 @@ __device__ __forceinline__ Raw<BF16> load_raw(const void* p, size_t at) {
       r.w[BF16 ? 0 : 4] = b.x, r.w[BF16 ? 1 : 5] = b.y, r.w[BF16 ? 2 : 6] = b.z, r.w[BF16 ? 3 : 7] = b.w;
     }
   } else if (BF16) {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + at;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.w[j] = (uint32_t)q[2 * j] | ((uint32_t)q[2 * j + 1] << 16);
   } else {
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + at;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
 #pragma unroll
     for (int j = 0; j < (BF16 ? 4 : 8); ++j) r.w[j] = q[j];
   }
@@ -83,7 +79,7 @@ __device__ __forceinline__ void unpack(const Raw<BF16>& r, float2 (&x)[4]) {
 }
 
 template <bool BF16, bool VEC>
-__device__ __forceinline__ void store8(void* p, size_t at, const float2 (&x)[4]) {
+__device__ __forceinline__ void store8(uint8_t* p, const float2 (&x)[4]) {
   if (BF16) {
     uint32_t w[4];
 #pragma unroll
@@ -91,7 +87,7 @@ __device__ __forceinline__ void store8(void* p, size_t at, const float2 (&x)[4])
       const __nv_bfloat162 h = __float22bfloat162_rn(x[j]);
       w[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    uint16_t* b = reinterpret_cast<uint16_t*>(p) + at;
+    uint16_t* b = reinterpret_cast<uint16_t*>(p);
     if (VEC) {
       *reinterpret_cast<uint4*>(b) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
@@ -99,7 +95,7 @@ __device__ __forceinline__ void store8(void* p, size_t at, const float2 (&x)[4])
       for (int j = 0; j < 8; ++j) b[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
     }
   } else {
-    float* f = reinterpret_cast<float*>(p) + at;
+    float* f = reinterpret_cast<float*>(p);
     if (VEC) {
       *reinterpret_cast<float4*>(f) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
       *reinterpret_cast<float4*>(f + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
@@ -111,7 +107,9 @@ __device__ __forceinline__ void store8(void* p, size_t at, const float2 (&x)[4])
 }
 
 __device__ __forceinline__ float row_sum(float s, int L) {
-  for (int off = L >> 1; off; off >>= 1) s += __shfl_xor_sync(FULL, s, off);
+#pragma unroll
+  for (int off = 16; off; off >>= 1)
+    if (off < L) s += __shfl_xor_sync(FULL, s, off);
   return s;
 }
 __device__ __forceinline__ float dot8(const float2 (&a)[4], const float2 (&b)[4]) {
@@ -128,58 +126,77 @@ __host__ __device__ inline Pairs pairs_of(const NormArgs& a) {
   if (a.interleaved) return a.rot % 8 == 0 ? PAIRS_LANE : PAIRS_ANY;
   return a.rot % 16 == 0 ? PAIRS_LANES : PAIRS_ANY;
 }
-// Place of pair i in a token's table.  A lane reads its 4 or 8 pairs two at a time; a step's reads of all lanes lie side
-// by side.
+// Place of pair i in the token's table.  A lane reads its 4 or 8 pairs two at a time; a step's reads of all lanes lie
+// side by side.
 __device__ __forceinline__ int pair_place(Pairs p, int half, int i) {
   if (p == PAIRS_LANE) return (((i & 3) >> 1) * (half >> 2) + (i >> 2)) * 2 + (i & 1);
   if (p == PAIRS_LANES) return (((i & 7) >> 1) * (half >> 3) + (i >> 3)) * 2 + (i & 1);
   return i;
 }
 
-// cos and sin of every pair's angle for `ntok` tokens from tok0 on: tab[token][place]
-__device__ __forceinline__ void angle_table(const NormArgs& a, Pairs p, float2* tab, int64_t tok0, int ntok) {
+// A token's turn as this lane applies it: y[j] -> y[j] * c[j] + (its mates) * s[j], the signs and channels that are not
+// turned (c = 1, s = 0) in c and s.
+struct Turn {
+  float2 c[4], s[4];
+  int mate;                // PAIRS_LANES: the lane that holds the mates
+};
+
+// cos and sin of every pair's angle at position `pos`, by the whole warp: into its table, from there into `turn`.  sgn: -1
+// turns back.  turns: inv_freq / 2 pi.
+__device__ __forceinline__ void set_turn(const NormArgs& a, Pairs p, Turn& t, float2* tab, const double* turns, int pos,
+                                         float sgn, int c, int lane) {
   const int half = a.rot >> 1;
-  for (int e = threadIdx.x; e < ntok * half; e += kThreads) {
-    const int lt = e / half, i = e - lt * half;
-    float2 cs = make_float2(1.f, 0.f);               // behind the last token: rows of zeros, turned by nothing
-    if (tok0 + lt < a.tokens) {
-      const double turns = (double)a.pos[tok0 + lt] * (double)a.inv_freq[i] * 0.15915494309189533577;
-      sincospif(2.f * (float)(turns - rint(turns)), &cs.y, &cs.x);
+  __syncwarp();
+  for (int i = lane; i < half; i += 32) {
+    const double x = (double)pos * turns[i];
+    float s, co;
+    sincospif(2.f * (float)(x - rint(x)), &s, &co);
+    tab[pair_place(p, half, i)] = make_float2(co, sgn * s);
+  }
+  __syncwarp();
+  if (p == PAIRS_ANY) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) t.c[j] = make_float2(1.f, 1.f), t.s[j] = make_float2(0.f, 0.f);
+  const float4* t4 = reinterpret_cast<const float4*>(tab);
+  if (p == PAIRS_LANE) {
+    if (8 * c < a.rot) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const float4 v = t4[(j >> 1) * (half >> 2) + c];
+        t.c[j] = make_float2(v.x, v.x), t.c[j + 1] = make_float2(v.z, v.z);
+        t.s[j] = make_float2(-v.y, v.y), t.s[j + 1] = make_float2(-v.w, v.w);
+      }
     }
-    tab[lt * half + pair_place(p, half, i)] = cs;
+  } else {
+    const int hl = half >> 3;
+    const bool low = c < hl, on = c < 2 * hl;
+    t.mate = (lane - c) + (low ? c + hl : (on ? c - hl : c));
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 v = t4[j * hl + (low ? c : c - hl)];
+        t.c[j] = make_float2(v.x, v.z);
+        t.s[j] = low ? make_float2(-v.y, -v.w) : make_float2(v.y, v.w);
+      }
+    }
   }
 }
 
-// Turns the row held by the lanes of this group by `sgn` times its angles.  c: the lane's place in its row; xch: shared
-// memory of 8 floats a thread, for pairs that lie anyhow.
-__device__ __forceinline__ void turn8(const NormArgs& a, Pairs p, float2 (&y)[4], const float2* t, float sgn, int c, float* xch) {
-  const int col = 8 * c, half = a.rot >> 1;
+// xch: shared memory of 8 floats a lane, for pairs that lie anyhow.
+__device__ __forceinline__ void turn8(const NormArgs& a, Pairs p, float2 (&y)[4], const Turn& t, const float2* tab, int c, int lane,
+                                      float* xch) {
   if (p == PAIRS_LANE) {
-    if (col < a.rot) {
-      const float4* t4 = reinterpret_cast<const float4*>(t) + c;
-      const int step = half >> 2;
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        const float4 cs = t4[(j >> 1) * step];
-        const float s0 = sgn * cs.y, s1 = sgn * cs.w;
-        y[j] = make_float2(y[j].x * cs.x - y[j].y * s0, y[j].y * cs.x + y[j].x * s0);
-        y[j + 1] = make_float2(y[j + 1].x * cs.z - y[j + 1].y * s1, y[j + 1].y * cs.z + y[j + 1].x * s1);
-      }
-    }
+    for (int j = 0; j < 4; ++j) y[j] = __ffma2_rn(make_float2(y[j].y, y[j].x), t.s[j], __fmul2_rn(y[j], t.c[j]));
   } else if (p == PAIRS_LANES) {
-    const int lane = threadIdx.x & 31, hl = half >> 3, base = lane - c;
-    const bool low = c < hl, on = c < 2 * hl;
-    const int mate = low ? c + hl : (on ? c - hl : c);
-    const float flip = low ? -sgn : sgn;
-    const float4* t4 = reinterpret_cast<const float4*>(t) + (low ? c : (on ? c - hl : 0));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float ox = __shfl_sync(FULL, y[j].x, base + mate), oy = __shfl_sync(FULL, y[j].y, base + mate);
-      const float4 cs = t4[j * hl];
-      if (on) y[j] = make_float2(y[j].x * cs.x + ox * (flip * cs.y), y[j].y * cs.z + oy * (flip * cs.w));
+      const float2 o = make_float2(__shfl_sync(FULL, y[j].x, t.mate), __shfl_sync(FULL, y[j].y, t.mate));
+      y[j] = __ffma2_rn(o, t.s[j], __fmul2_rn(y[j], t.c[j]));
     }
   } else {
-    float* mine = xch + (size_t)(threadIdx.x - c) * 8;    // the row, 8 L floats
+    const int col = 8 * c, half = a.rot >> 1;
+    float* mine = xch + (size_t)(lane - c) * 8;           // the row, 8 L floats
 #pragma unroll
     for (int j = 0; j < 4; ++j) mine[col + 2 * j] = y[j].x, mine[col + 2 * j + 1] = y[j].y;
     __syncwarp();
@@ -192,8 +209,8 @@ __device__ __forceinline__ void turn8(const NormArgs& a, Pairs p, float2 (&y)[4]
         const int i = a.interleaved ? x >> 1 : (x < half ? x : x - half);
         const bool first = a.interleaved ? !(x & 1) : x < half;
         const float other = mine[a.interleaved ? x ^ 1 : (first ? x + half : x - half)];
-        const float2 cs = t[i];
-        z[j] = z[j] * cs.x + other * ((first ? -sgn : sgn) * cs.y);
+        const float2 cs = tab[i];
+        z[j] = z[j] * cs.x + other * (first ? -cs.y : cs.y);
       }
     }
     __syncwarp();
@@ -202,134 +219,158 @@ __device__ __forceinline__ void turn8(const NormArgs& a, Pairs p, float2 (&y)[4]
   }
 }
 
-// Where row x of a tile lies.
-struct Row {
-  bool in;                  // there is such a row and this lane holds a part of it
-  int side, head, ltok;
-  int64_t tok;
+// How the work is cut: units of one token and one of `parts` equal shares of its batches.
+struct NormUnits {
+  int32_t L;                // lanes a row
+  int32_t batches[2];       // of a token's queries, of its keys: U rows a lane each
+  int32_t parts, share;     // batches a part
+  int64_t units;
 };
-__device__ __forceinline__ Row locate(const NormArgs& a, const NormTiles& n, int64_t tok0, int x, int c) {
-  Row r;
-  r.ltok = n.R > 1 ? (int)__umulhi((uint32_t)x, n.magic) : x;
-  const int row = x - r.ltok * n.R;
-  r.side = row >= a.side[0].heads;
-  r.head = r.side ? row - a.side[0].heads : row;
-  r.tok = tok0 + r.ltok;
-  r.in = r.ltok < n.tokens && r.tok < a.tokens && 8 * c < a.D;
-  if (r.ltok >= n.tokens) r.ltok = n.tokens - 1;
-  return r;
-}
 
-// BACK 0: the operator; 1: its gradient; 2: with the weights' gradients.  U rows a thread and tile.
-template <bool BF16, bool VEC, int U, int BACK>
-__global__ void __launch_bounds__(kThreads, 2) qk_norm_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ NormTiles n) {
-  extern __shared__ __align__(16) float2 shared[];
+// BACK 0: the operator; 1: its gradient; 2: with the weights' gradients.  U rows a lane and batch.  LL: lanes a row (0:
+// as `n` says).
+template <bool BF16, bool VEC, int LL, int U, int BACK>
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ NormUnits n) {
+  constexpr int E = BF16 ? 2 : 4;
+  __shared__ double turns[kMaxD / 2];
+  __shared__ __align__(16) float2 tabs[kWarps][kMaxD / 2];
+  __shared__ float xch[kWarps][256];
   const Pairs pairs = pairs_of(a);
-  const int L = n.L, c = threadIdx.x & (L - 1), slots = kThreads / L, slot = threadIdx.x / L;
-  const int tab_size = n.tokens * (a.rot >> 1) + ((n.tokens * (a.rot >> 1)) & 1);
-  float2* tab[2] = {shared, shared + tab_size};
-  float* xch = reinterpret_cast<float*>(shared + 2 * tab_size);
-  float2 w[2][4];
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[s][j] = make_float2(1.f, 1.f);
-      if (a.side[s].w && 8 * c < a.D) w[s][j] = make_float2(a.side[s].w[8 * c + 2 * j], a.side[s].w[8 * c + 2 * j + 1]);
-    }
+  const int L = LL ? LL : n.L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & (L - 1), sub = lane / L, RPI = 32 / L;
+  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) turns[i] = (double)a.inv_freq[i] * 0.15915494309189533577;
+  __syncthreads();
+  const bool held = 8 * c < a.D;
   float2 dw[2][4];
   if (BACK == 2) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[0][j] = dw[1][j] = make_float2(0.f, 0.f);
   }
-  auto first_token = [&](int64_t tile, int* x0) {
-    const int64_t group = n.passes > 1 ? tile / n.passes : tile;
-    *x0 = (int)(tile - group * n.passes) * (slots * U) + slot;
-    return group * n.tokens;
+  // a batch: rows RPI (U b + u) + sub of one side of one token
+  struct Batch {
+    int64_t unit;
+    int tok, side, b, left;          // left: batches of the unit from this one on
+  };
+  auto begin = [&](Batch& x) {       // the first batch of x.unit
+    const int64_t tok = n.parts > 1 ? x.unit / n.parts : x.unit;
+    int b = (int)(x.unit - tok * n.parts) * n.share;
+    x.tok = (int)tok;
+    x.left = min(n.share, n.batches[0] + n.batches[1] - b);
+    x.side = b >= n.batches[0];
+    x.b = x.side ? b - n.batches[0] : b;
+  };
+  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  auto advance = [&](Batch& x) {     // false behind the last
+    if (--x.left > 0) {
+      if (++x.b == (x.side ? n.batches[1] : n.batches[0])) {
+        x.b = 0;
+        x.side = 1;
+      }
+      return true;
+    }
+    x.unit += warps;
+    if (x.unit >= n.units) return false;
+    begin(x);
+    return x.left > 0;
   };
   Raw<BF16> nx[U], ng[BACK ? U : 1];
-  auto fetch = [&](int64_t tile) {
-    int x0;
-    const int64_t tok0 = first_token(tile, &x0);
+  int npos = 0;
+  auto fetch = [&](const Batch& x) {
+    const NormSide& s = a.side[x.side];
+    const uint8_t* px = reinterpret_cast<const uint8_t*>(s.x) + (x.tok * s.x_stride + 8 * c) * E;
+    const uint8_t* pg = reinterpret_cast<const uint8_t*>(s.dy) + ((int64_t)x.tok * s.heads * a.D + 8 * c) * E;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Row r = locate(a, n, tok0, x0 + u * slots, c);
-      const NormSide& s = a.side[r.side];
+      const int row = RPI * (U * x.b + u) + sub;
       nx[u] = zero_raw<BF16>();
       if (BACK) ng[BACK ? u : 0] = zero_raw<BF16>();
-      if (r.in) {
-        nx[u] = load_raw<BF16, VEC>(s.x, (size_t)(r.tok * s.x_stride) + (size_t)r.head * a.D + 8 * c);
-        if (BACK) ng[BACK ? u : 0] = load_raw<BF16, VEC>(s.dy, (size_t)(r.tok * s.heads + r.head) * a.D + 8 * c);
+      if (row < s.heads && held) {
+        nx[u] = load_raw<BF16, VEC>(px + row * a.D * E);
+        if (BACK) ng[BACK ? u : 0] = load_raw<BF16, VEC>(pg + row * a.D * E);
       }
     }
-    return tok0;
+    if (pairs != PAIRS_NONE) npos = a.pos[x.tok];
   };
-  int64_t tile = blockIdx.x;
-  int64_t tok0 = fetch(tile);
-  int cur = 0;
-  if (pairs != PAIRS_NONE) {
-    angle_table(a, pairs, tab[0], tok0, n.tokens);
-    __syncthreads();
+  Batch cur;
+  cur.unit = (int64_t)blockIdx.x * kWarps + warp;
+  bool more = cur.unit < n.units;
+  if (more) {
+    begin(cur);
+    more = cur.left > 0;
   }
-  for (; tile < n.tiles; tile += gridDim.x, cur ^= 1) {
+  if (more) fetch(cur);
+  Turn turn;
+  int turned = -1, weighted = -1;    // the token of `turn`, the side of `w`
+  float2 w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = make_float2(1.f, 1.f);
+  while (more) {
+    const Batch now = cur;
     Raw<BF16> rx[U], rg[BACK ? U : 1];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       rx[u] = nx[u];
       if (BACK) rg[BACK ? u : 0] = ng[BACK ? u : 0];
     }
-    int x0;
-    tok0 = first_token(tile, &x0);
-    const bool more = tile + gridDim.x < n.tiles;
-    if (more) {
-      const int64_t next = fetch(tile + gridDim.x);
-      if (pairs != PAIRS_NONE) angle_table(a, pairs, tab[cur ^ 1], next, n.tokens);
+    const int pos = npos;
+    more = advance(cur);
+    if (more) fetch(cur);
+    const NormSide& s = a.side[now.side];
+    if (pairs != PAIRS_NONE && now.tok != turned) {
+      set_turn(a, pairs, turn, tabs[warp], turns, pos, BACK ? -1.f : 1.f, c, lane);
+      turned = now.tok;
     }
+    if (now.side != weighted) {
+      weighted = now.side;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = s.w && held ? make_float2(s.w[8 * c + 2 * j], s.w[8 * c + 2 * j + 1]) : make_float2(1.f, 1.f);
+    }
+    uint8_t* py = reinterpret_cast<uint8_t*>(s.y) + (now.tok * s.y_stride + 8 * c) * E;
+    const float scale = s.scale;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Row r = locate(a, n, tok0, x0 + u * slots, c);
-      const NormSide& s = a.side[r.side];
-      const float2* t = tab[cur] + r.ltok * (a.rot >> 1);
-      const size_t at = (size_t)(r.tok * s.y_stride) + (size_t)r.head * a.D + 8 * c;
-      float2 x[4], ww[4];
+      const int row = RPI * (U * now.b + u) + sub;
+      const bool in = row < s.heads && held;
+      float2 x[4];
       unpack<BF16>(rx[u], x);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ww[j] = r.side ? w[1][j] : w[0][j];
       const float rr = rsqrtf(fmaf(row_sum(dot8(x, x), L), a.inv_n, a.eps));
       if (!BACK) {
-        const float2 f = make_float2(rr * s.scale, rr * s.scale);
+        const float2 f = make_float2(rr * scale, rr * scale);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(__fmul2_rn(x[j], f), ww[j]);
-        if (pairs != PAIRS_NONE) turn8(a, pairs, x, t, 1.f, c, xch);
-        if (r.in) store8<BF16, VEC>(s.y, at, x);
+        for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(__fmul2_rn(x[j], f), w[j]);
+        if (pairs != PAIRS_NONE) turn8(a, pairs, x, turn, tabs[warp], c, lane, xch[warp]);
+        if (in) store8<BF16, VEC>(py + row * a.D * E, x);
       } else {
         float2 g[4];
         unpack<BF16>(rg[BACK ? u : 0], g);
-        if (pairs != PAIRS_NONE) turn8(a, pairs, g, t, -1.f, c, xch);
-        const float2 r2 = make_float2(rr, rr), sc = make_float2(s.scale, s.scale);
+        if (pairs != PAIRS_NONE) turn8(a, pairs, g, turn, tabs[warp], c, lane, xch[warp]);
+        const float2 r2 = make_float2(rr, rr), sc = make_float2(scale, scale);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           x[j] = __fmul2_rn(x[j], r2);                          // x^
           g[j] = __fmul2_rn(g[j], sc);                          // u
-          if (BACK == 2) {
-            const float2 z = make_float2(0.f, 0.f);
-            const float2 keep = r.in ? x[j] : z;
-            dw[0][j] = __ffma2_rn(r.side ? z : keep, g[j], dw[0][j]);
-            dw[1][j] = __ffma2_rn(r.side ? keep : z, g[j], dw[1][j]);
-          }
-          g[j] = __fmul2_rn(g[j], ww[j]);                       // h
         }
+        if (BACK == 2) {                                        // rows that are not there are zeros
+          if (now.side) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dw[1][j] = __ffma2_rn(x[j], g[j], dw[1][j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dw[0][j] = __ffma2_rn(x[j], g[j], dw[0][j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(g[j], w[j]);      // h
         const float d = row_sum(dot8(x, g), L) * -a.inv_n;
         const float2 d2 = make_float2(d, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(r2, __ffma2_rn(x[j], d2, g[j]));
-        if (r.in) store8<BF16, VEC>(s.y, at, g);
+        if (in) store8<BF16, VEC>(py + row * a.D * E, g);
       }
     }
-    if (pairs != PAIRS_NONE && more) __syncthreads();           // the next table is whole, this one is done with
   }
   if (BACK == 2) {
-    // this block's sums over its row slots, in the order of the slots
+    // this block's sums over its rows, in the order of the warps and of the rows a warp holds
     __shared__ float2 red[kThreads * 4];
     for (int side = 0; side < 2; ++side) {
       __syncthreads();
@@ -337,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_kernel(const __grid_const
       for (int j = 0; j < 4; ++j) red[threadIdx.x * 4 + j] = dw[side][j];
       __syncthreads();
       for (int col = threadIdx.x; col < a.D; col += kThreads) {
-        float s = 0.f;
-        for (int k = 0; k < slots; ++k) s += reinterpret_cast<const float*>(red)[k * L * 8 + col];
-        a.partial[((size_t)blockIdx.x * 2 + side) * a.D + col] = s;
+        float sum = 0.f;
+        for (int k = 0; k < kWarps * RPI; ++k) sum += reinterpret_cast<const float*>(red)[k * L * 8 + col];
+        a.partial[((size_t)blockIdx.x * 2 + side) * a.D + col] = sum;
       }
     }
   }
@@ -375,44 +416,39 @@ bool aligned16(const NormArgs& a, bool back) {
   return true;
 }
 
-// Tiles of `per` rows: as many whole tokens as fit, or a part of one.
-NormTiles tiles_of(const NormArgs& a, int per) {
-  NormTiles n;
+template <bool BF16, bool VEC, int LL, int BACK>
+cudaError_t launch_l(const NormArgs& a, cudaStream_t st, int* blocks_out) {
+  constexpr int U = BACK ? (BF16 ? 2 : 1) : (BF16 ? 4 : 2);
+  NormUnits n;
   n.L = lanes_of(a.D);
-  n.R = a.side[0].heads + a.side[1].heads;
-  n.magic = n.R > 1 ? (uint32_t)((((uint64_t)1 << 32) + n.R - 1) / n.R) : 0;
-  n.tokens = per >= n.R ? per / n.R : 1;
-  n.passes = per >= n.R ? 1 : (n.R + per - 1) / per;
-  n.tiles = ((int64_t)a.tokens + n.tokens - 1) / n.tokens * n.passes;
-  return n;
-}
-
-size_t shared_bytes(const NormArgs& a, const NormTiles& n) {
-  const size_t t = (size_t)n.tokens * (a.rot / 2);
-  return 2 * (t + (t & 1)) * sizeof(float2) + (pairs_of(a) == PAIRS_ANY ? kThreads * 8 * sizeof(float) : 0);
-}
-
-template <bool BF16, bool VEC, int U, int BACK>
-cudaError_t launch_u(const NormArgs& a, cudaStream_t st, int* blocks_out) {
-  const NormTiles n = tiles_of(a, kThreads / lanes_of(a.D) * U);
-  const size_t smem = shared_bytes(a, n);
-  const int64_t most = kBlocks;
-  const int blocks = (int)(n.tiles < most ? n.tiles : most);
+  const int per = 32 / n.L * U;
+  n.batches[0] = (a.side[0].heads + per - 1) / per;
+  n.batches[1] = (a.side[1].heads + per - 1) / per;
+  const int all = n.batches[0] + n.batches[1];
+  // a token a warp; in parts where that leaves warps without work
+  const int64_t warps = (int64_t)kBlocks * kWarps;
+  int64_t parts = a.tokens >= warps ? 1 : warps / a.tokens;
+  if (parts > all) parts = all;
+  n.share = (int32_t)((all + parts - 1) / parts);
+  n.parts = (all + n.share - 1) / n.share;
+  n.units = (int64_t)a.tokens * n.parts;
+  const int64_t need = (n.units + kWarps - 1) / kWarps;
+  const int blocks = (int)(need < kBlocks ? need : kBlocks);
   if (blocks_out) *blocks_out = blocks;
-  if (smem > 48 * 1024) {          // small heads in fp32 rows of one token each: tables of 32 KB and more
-    const cudaError_t e = cudaFuncSetAttribute(qk_norm_kernel<BF16, VEC, U, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  qk_norm_kernel<BF16, VEC, U, BACK><<<blocks, kThreads, smem, st>>>(a, n);
+  qk_norm_kernel<BF16, VEC, LL, U, BACK><<<blocks, kThreads, 0, st>>>(a, n);
   return cudaGetLastError();
 }
 
-// U rows a thread where that still gives every SM some blocks, else one.
 template <bool BF16, bool VEC, int BACK>
-cudaError_t launch_t(const NormArgs& a, int64_t rows, cudaStream_t st, int* blocks) {
-  constexpr int U = BACK ? (BF16 ? 2 : 1) : (BF16 ? 4 : 2);
-  if (U == 1 || rows * lanes_of(a.D) / (kThreads * U) < 2 * kSms) return launch_u<BF16, VEC, 1, BACK>(a, st, blocks);
-  return launch_u<BF16, VEC, U, BACK>(a, st, blocks);
+cudaError_t launch_t(const NormArgs& a, int64_t, cudaStream_t st, int* blocks) {
+  if (VEC) {
+    switch (lanes_of(a.D)) {
+      case 8: return launch_l<BF16, VEC, 8, BACK>(a, st, blocks);
+      case 16: return launch_l<BF16, VEC, 16, BACK>(a, st, blocks);
+      case 32: return launch_l<BF16, VEC, 32, BACK>(a, st, blocks);
+    }
+  }
+  return launch_l<BF16, VEC, 0, BACK>(a, st, blocks);
 }
 
 template <int BACK>
