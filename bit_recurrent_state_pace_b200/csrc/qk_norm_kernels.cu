@@ -8,7 +8,7 @@
 // number of instructions a row.  A row (one head of one token) is held by L lanes of a warp, 8 elements (one 16-byte load
 // in bf16) each, so a warp's loads are full lines and both sums are shuffles.  A warp takes a token (or, where there are
 // few, a part of one) and goes through its queries, then its keys, U rows a lane at a time with the next ones' loads in
-// flight: a lane keeps its columns, so the weights, and the token's cosines and sines, stay in registers.  The angle
+// flight (asynchronous copies to shared memory: four batches, where registers held one): a lane keeps its columns, so the weights, and the token's cosines and sines, stay in registers.  The angle
 // pos * inv_freq / 2 pi is taken in fp64 and only its fraction goes on in fp32: far positions lose nothing.
 //
 // Blocks with one table of angles for their tokens, rows in a flat list, took 174 instructions a row (this: about 80) and
@@ -24,6 +24,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSms = 148;                  // B200
 constexpr int kBlocks = kSms * 2;          // resident: two an SM
 constexpr int kMaxD = 256;
+constexpr int kStages = 4;
 
 // lanes that hold a row: the power of two that gives each at most 8 elements
 inline int lanes_of(int D) {
@@ -38,36 +39,46 @@ struct Raw {
   uint32_t w[BF16 ? 4 : 8];
 };
 
+// A lane's eight elements of a row into its own place of shared memory (16 bytes a thread and step of kThreads), by
+// asynchronous copies where the addresses allow; zeros where there is no such row.
 template <bool BF16, bool VEC>
-__device__ __forceinline__ Raw<BF16> load_raw(const uint8_t* p) {
-  Raw<BF16> r;
+__device__ __forceinline__ void copy_in(uint4* to, const uint8_t* p, bool in) {
   if (VEC) {
-    const uint4* q = reinterpret_cast<const uint4*>(p);
-    const uint4 a = q[0];
-    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
-    if (!BF16) {
-      const uint4 b = q[1];
-      r.w[BF16 ? 0 : 4] = b.x, r.w[BF16 ? 1 : 5] = b.y, r.w[BF16 ? 2 : 6] = b.z, r.w[BF16 ? 3 : 7] = b.w;
-    }
-  } else if (BF16) {
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = (uint32_t)q[2 * j] | ((uint32_t)q[2 * j + 1] << 16);
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to + h * kThreads)),
+                   "l"(p + 16 * h), "r"(in ? 16 : 0)
+                   : "memory");
   } else {
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+    uint32_t w[BF16 ? 4 : 8];
 #pragma unroll
-    for (int j = 0; j < (BF16 ? 4 : 8); ++j) r.w[j] = q[j];
+    for (int j = 0; j < (BF16 ? 4 : 8); ++j) {
+      w[j] = 0u;
+      if (!in) continue;
+      if (BF16) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * j;
+        w[j] = (uint32_t)q[0] | ((uint32_t)q[1] << 16);
+      } else {
+        w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h) to[h * kThreads] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> copied(const uint4* from) {
+  Raw<BF16> r;
+#pragma unroll
+  for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+    const uint4 v = from[h * kThreads];
+    r.w[4 * h] = v.x, r.w[4 * h + 1] = v.y, r.w[4 * h + 2] = v.z, r.w[4 * h + 3] = v.w;
   }
   return r;
 }
-
-template <bool BF16>
-__device__ __forceinline__ Raw<BF16> zero_raw() {
-  Raw<BF16> r;
-#pragma unroll
-  for (int j = 0; j < (BF16 ? 4 : 8); ++j) r.w[j] = 0u;
-  return r;
-}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <bool BF16>
 __device__ __forceinline__ void unpack(const Raw<BF16>& r, float2 (&x)[4]) {
@@ -272,32 +283,44 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_kernel(const __grid_const
     begin(x);
     return x.left > 0;
   };
-  Raw<BF16> nx[U], ng[BACK ? U : 1];
-  int npos = 0;
-  auto fetch = [&](const Batch& x) {
+  // batches on their way: kStages - 1 ahead of the one worked on.  A lane reads what it copied itself, so that nothing
+  // but its own copies is waited for.
+  extern __shared__ __align__(16) uint4 staged[];
+  constexpr int kRow = BF16 ? 1 : 2, kStage = (BACK ? 2 : 1) * U * kRow * kThreads;       // in 16 bytes
+  auto fetch = [&](const Batch& x, int stage) {
+    uint4* to = staged + stage * kStage + threadIdx.x;
     const NormSide& s = a.side[x.side];
     const uint8_t* px = reinterpret_cast<const uint8_t*>(s.x) + (x.tok * s.x_stride + 8 * c) * E;
     const uint8_t* pg = reinterpret_cast<const uint8_t*>(s.dy) + ((int64_t)x.tok * s.heads * a.D + 8 * c) * E;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int row = RPI * (U * x.b + u) + sub;
-      nx[u] = zero_raw<BF16>();
-      if (BACK) ng[BACK ? u : 0] = zero_raw<BF16>();
-      if (row < s.heads && held) {
-        nx[u] = load_raw<BF16, VEC>(px + row * a.D * E);
-        if (BACK) ng[BACK ? u : 0] = load_raw<BF16, VEC>(pg + row * a.D * E);
-      }
+      const bool in = row < s.heads && held;
+      copy_in<BF16, VEC>(to + u * kRow * kThreads, px + row * a.D * E, in);
+      if (BACK) copy_in<BF16, VEC>(to + (U + u) * kRow * kThreads, pg + row * a.D * E, in);
     }
-    if (pairs != PAIRS_NONE) npos = a.pos[x.tok];
+    return pairs != PAIRS_NONE ? a.pos[x.tok] : 0;
   };
-  Batch cur;
+  Batch cur, ahead;
   cur.unit = (int64_t)blockIdx.x * kWarps + warp;
   bool more = cur.unit < n.units;
   if (more) {
     begin(cur);
     more = cur.left > 0;
   }
-  if (more) fetch(cur);
+  ahead = cur;
+  bool to_fetch = more;
+  int pos[kStages - 1];              // positions of the batches on their way
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) {
+    pos[k] = 0;
+    if (to_fetch) {
+      pos[k] = fetch(ahead, k);
+      to_fetch = advance(ahead);
+    }
+    copies_commit();
+  }
+  int stage = 0;
   Turn turn;
   int turned = -1, weighted = -1;    // the token of `turn`, the side of `w`
   float2 w[4];
@@ -305,18 +328,21 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_kernel(const __grid_const
   for (int j = 0; j < 4; ++j) w[j] = make_float2(1.f, 1.f);
   while (more) {
     const Batch now = cur;
-    Raw<BF16> rx[U], rg[BACK ? U : 1];
+    copies_wait<kStages - 2>();
+    const int at = pos[0];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rx[u] = nx[u];
-      if (BACK) rg[BACK ? u : 0] = ng[BACK ? u : 0];
+    for (int k = 0; k + 2 < kStages; ++k) pos[k] = pos[k + 1];
+    if (to_fetch) {                  // into the stage worked on last
+      pos[kStages - 2] = fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
+      to_fetch = advance(ahead);
     }
-    const int pos = npos;
+    copies_commit();
+    const uint4* from = staged + stage * kStage + threadIdx.x;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
     more = advance(cur);
-    if (more) fetch(cur);
     const NormSide& s = a.side[now.side];
     if (pairs != PAIRS_NONE && now.tok != turned) {
-      set_turn(a, pairs, turn, tabs[warp], turns, pos, BACK ? -1.f : 1.f, c, lane);
+      set_turn(a, pairs, turn, tabs[warp], turns, at, BACK ? -1.f : 1.f, c, lane);
       turned = now.tok;
     }
     if (now.side != weighted) {
@@ -332,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_kernel(const __grid_const
       const int row = RPI * (U * now.b + u) + sub;
       const bool in = row < s.heads && held;
       float2 x[4];
-      unpack<BF16>(rx[u], x);
+      unpack<BF16>(copied<BF16>(from + u * kRow * kThreads), x);
       const float rr = rsqrtf(fmaf(row_sum(dot8(x, x), L), a.inv_n, a.eps));
       if (!BACK) {
         const float2 f = make_float2(rr * scale, rr * scale);
@@ -342,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_kernel(const __grid_const
         if (in) store8<BF16, VEC>(py + row * a.D * E, x);
       } else {
         float2 g[4];
-        unpack<BF16>(rg[BACK ? u : 0], g);
+        unpack<BF16>(copied<BF16>(from + (U + u) * kRow * kThreads), g);
         if (pairs != PAIRS_NONE) turn8(a, pairs, g, turn, tabs[warp], c, lane, xch[warp]);
         const float2 r2 = make_float2(rr, rr), sc = make_float2(scale, scale);
 #pragma unroll
@@ -435,7 +461,10 @@ cudaError_t launch_l(const NormArgs& a, cudaStream_t st, int* blocks_out) {
   const int64_t need = (n.units + kWarps - 1) / kWarps;
   const int blocks = (int)(need < kBlocks ? need : kBlocks);
   if (blocks_out) *blocks_out = blocks;
-  qk_norm_kernel<BF16, VEC, LL, U, BACK><<<blocks, kThreads, 0, st>>>(a, n);
+  const int smem = kStages * (BACK ? 2 : 1) * U * (BF16 ? 1 : 2) * kThreads * 16;
+  const cudaError_t e = cudaFuncSetAttribute(qk_norm_kernel<BF16, VEC, LL, U, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  qk_norm_kernel<BF16, VEC, LL, U, BACK><<<blocks, kThreads, smem, st>>>(a, n);
   return cudaGetLastError();
 }
 
