@@ -19,11 +19,11 @@
 // rounding).  P is split into two bf16 parts (16 bits): rounded to one, short prompts came 1.5 times as far from the
 // exact outputs as those rounded once.  The value times its decay is split into three (24 bits), so that the states,
 // which are fp32 outputs and run over the whole sequence, are summed from exact products of 24 bits; two parts would
-// leave about 2e-6 of the state.
+// leave about 2e-6 of the state, and are taken in a backward pass without dS0 (a third of U's products and of the split).
 //
 // One persistent CTA of 28 warps per SM, each group of four (a TMEM lane quadrant each) with one job, so that their
 // latencies overlap:
-//  * warp 0: loads the chunks' tiles by TMA, three chunks ahead; warp 1: issues the products;
+//  * warp 0: loads the chunks' tiles by TMA, a chunk ahead; warp 1: issues the products; warp 2: the states by TMA;
 //  * warps 4-11: the value's decayed parts into TMEM, half of the tokens each four;
 //  * warps 12-15: P from SC;  warps 16-19: the output, stored by TMA;
 //  * warps 20-27: the state, half of the key channels each four.
@@ -44,18 +44,22 @@ constexpr int C = 64;                 // tokens a chunk
 constexpr int NST = 3;                // staged chunks
 constexpr int kTcThreads = 896;
 constexpr int kSms = 148;             // B200
+constexpr int kMaxSorted = 512;       // sequences that are put in order (more come out even anyway)
 
 // TMEM columns.  All 512 are allocated, so the allocation begins at column 0.
 constexpr uint32_t T_SC = 0, T_OI = 64, T_OP = 128, T_U = 192, T_S = 320, T_V = 384;
 
-struct LinMaps { CUtensorMap in[4], out[kLinMaxWalks]; };
+struct LinMaps {
+  CUtensorMap in[4], out[kLinMaxWalks];              // the packed tensors
+  CUtensorMap s_in[kLinMaxWalks], s_out[kLinMaxWalks], ws;   // states: rows of D fp32
+};
 
 struct LinTc {
   LinArgs a;
   int32_t map_q[kLinMaxWalks], map_k[kLinMaxWalks], map_v[kLinMaxWalks];
   LinSplit split;
   float* ws;               // [walks][N][H][stretches][D][D]: each stretch's state
-  int32_t items;
+  int32_t items;           // of one walk: (n, h, stretch)
 };
 
 template <int D>
@@ -63,14 +67,18 @@ struct alignas(1024) LinSmem {
   static constexpr int TILE = C * D * 2;                 // D / 64 blocks of 64 rows of 128 bytes
   uint8_t stage[NST][3][TILE];                           // query | key | value
   uint8_t p[2][C * 128];                                 // P[i][j] in two bf16 parts, 128-byte swizzle
-  uint8_t o[2][TILE];                                    // output tiles on their way to memory: 64 rows of 32 channels a warp
+  static constexpr int STATE = D * D * 2;                // half of a state (D / 2 key channels)
+  uint8_t st[STATE];                                     // states on their way in and out: rows of 128 bytes, swizzled
+  uint8_t o[TILE];                                       // output tile on its way to memory: 64 rows of 32 channels a warp
   // tables of the decay, of two items in turn, each group of warps its own:
   float wv[2][2][2][C];                                  // warps 4-7, 8-11: decay of a token's value in the state behind a
                                                          // full chunk, and behind the sequence's last one (zeros beyond it)
   float pz[2][2 * C + 8];                                // warps 12-15: A^n at [C + n], zeros below
   float wo[2][2][C];                                     // warps 16-19: of the state in a token's output, as wv
   uint64_t full[NST], empty[NST];
-  uint64_t sc_full, p_full, v_full, s_full, u_full, u_empty, op_full, o_empty, drain;
+  uint64_t sc_full, p_full, v_full, s_full, u_full, u_empty, op_full, o_empty, st_full[2], st_done[2], drain;
+  int chunks[kMaxSorted];                                // of each sequence
+  uint16_t order[kMaxSorted];                            // sequences, the longest first
   uint32_t taddr;
 };
 
@@ -90,22 +98,31 @@ struct Item {
   __device__ __forceinline__ int rows(int c) const { return min(C, len - c * C); }
 };
 
+// The k-th item of this block (order_sequences says which those are), for k < item_rounds.
+__device__ __forceinline__ int item_rounds(const LinTc& t) {
+  const int groups = gridDim.x / t.a.walks;
+  return (t.items + groups - 1) / groups;
+}
 template <bool STATE_ONLY>
-__device__ __forceinline__ Item item_of(const LinTc& t, int x) {
+__device__ __forceinline__ Item item_of(const LinTc& t, const uint16_t* order, int k) {
+  const int groups = gridDim.x / t.a.walks, b = blockIdx.x / t.a.walks;
+  int x = k * groups + ((k & 1) ? groups - 1 - b : b);
   Item it;
-  it.w = x % t.a.walks;
-  x /= t.a.walks;
+  const bool there = x < t.items;
+  if (!there) x = 0;
+  it.w = t.a.walks > 1 ? blockIdx.x % t.a.walks : 0;
   it.seg = x % t.split.stretches;
   x /= t.split.stretches;
   it.h = x % t.a.H;
   it.n = x / t.a.H;
+  if (t.a.cu && t.a.N <= kMaxSorted) it.n = order[it.n];
   int end;
   seq_rows(t.a, it.n, &it.begin, &end);
   it.len = end - it.begin;
   const int nc = (it.len + C - 1) / C;
   int ns = (nc + t.split.per - 1) / t.split.per;
   it.nseg = ns < 1 ? 1 : (ns > t.split.stretches ? t.split.stretches : ns);
-  it.on = it.seg < it.nseg;
+  it.on = there && it.seg < it.nseg;
   // the stretch that a walk ends with hands its state to no other
   if (STATE_ONLY) it.on = it.on && it.seg != (t.a.walk[it.w].back ? 0 : it.nseg - 1);
   it.c0 = it.seg * t.split.per;
@@ -113,21 +130,69 @@ __device__ __forceinline__ Item item_of(const LinTc& t, int x) {
   if (!it.on) it.c0 = it.c1 = 0;
   return it;
 }
+// index of a stretch's state in ws, in states
+__device__ __forceinline__ int stretch_index(const LinTc& t, const Item& it) {
+  return ((it.w * t.a.N + it.n) * t.a.H + it.h) * t.split.stretches + it.seg;
+}
 __device__ __forceinline__ float* stretch_state(const LinTc& t, const Item& it) {
-  return t.ws + (((size_t)it.w * t.a.N + it.n) * t.a.H + it.h) * t.split.stretches * t.a.D * t.a.D +
-         (size_t)it.seg * t.a.D * t.a.D;
+  return t.ws + (size_t)stretch_index(t, it) * t.a.D * t.a.D;
+}
+// What an item begins from and leaves: a state of ws, of the walk's tensors (transposed or not), or none.
+struct StateIo {
+  bool in, out, in_swap, out_swap;
+};
+template <bool STATE_ONLY>
+__device__ __forceinline__ StateIo state_io(const LinTc& t, const Item& it) {
+  const LinWalk& w = t.a.walk[it.w];
+  StateIo io;
+  const bool cut = it.nseg > 1;
+  io.in = !STATE_ONLY && (cut || w.S_in);
+  io.in_swap = !cut && w.swap;
+  io.out = STATE_ONLY || (w.S_out && it.seg == (w.back ? 0 : it.nseg - 1));
+  io.out_swap = !STATE_ONLY && w.swap;
+  return io;
+}
+// The state's place in shared memory is exchanged in one go (the last item's state out, this one's in) where both lie
+// alike; else the one leaves before the other comes.
+__device__ __forceinline__ bool two_rounds(const StateIo& last, const StateIo& now) {
+  return last.out && now.in && last.out_swap != now.in_swap;
 }
 // k-th chunk of an item in its walk's order
 __device__ __forceinline__ int chunk_at(const Item& it, bool back, int k) { return back ? it.c1 - 1 - k : it.c0 + k; }
 
+// ---- which items a block takes ------------------------------------------------------
+// A walk's items (sequence, head, stretch) are dealt to its blocks in turn, back and forth, the longest sequences first
+// where lengths differ: the heads of a sequence run at the same time, so that their parts of a token's row are read
+// together, and the blocks' sums come out about even.  (Dealt in the order given, 64 prompts of 1 to 1021 tokens kept
+// some blocks busy twice as long as the mean; contiguous shares of equal cost were a fifth slower than that.)  Blocks
+// b, b + 1, b + 2 of a backward pass take the same heads in its three walks, which read the same tensors.
+template <int D>
+__device__ void order_sequences(const LinTc& t, LinSmem<D>& sm) {
+  if (!t.a.cu || t.a.N > kMaxSorted) return;
+  for (int n = threadIdx.x; n < t.a.N; n += kTcThreads) {
+    int begin, end;
+    seq_rows(t.a, n, &begin, &end);
+    sm.chunks[n] = (end - begin + C - 1) / C;
+  }
+  __syncthreads();
+  for (int n = threadIdx.x; n < t.a.N; n += kTcThreads) {
+    const int own = sm.chunks[n];
+    int rank = 0;
+    for (int m = 0; m < t.a.N; ++m) {
+      const int c = sm.chunks[m];
+      rank += c > own || (c == own && m < n);
+    }
+    sm.order[rank] = (uint16_t)n;
+  }
+}
 // ---- loads ---------------------------------------------------------------------
-template <int D, bool STATE_ONLY>
+template <int D, int PARTS, bool STATE_ONLY>
 __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
   using SM = LinSmem<D>;
   int k = 0;
   bool ok = true;
-  for (int x = blockIdx.x; x < t.items && ok; x += gridDim.x) {
-    const Item it = item_of<STATE_ONLY>(t, x);
+  for (int i = 0; i < item_rounds(t) && ok; ++i) {
+    const Item it = item_of<STATE_ONLY>(t, sm.order, i);
     const bool back = t.a.walk[it.w].back;
     const CUtensorMap* mp[3] = {&maps.in[t.map_q[it.w]], &maps.in[t.map_k[it.w]], &maps.in[t.map_v[it.w]]};
     for (int c = 0; c < it.chunks(); ++c, ++k) {
@@ -150,11 +215,80 @@ __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
   }
 }
 
+// ---- states ---------------------------------------------------------------------
+// One place in shared memory serves the states of all items, a half (the key channels of one group of the state's warps)
+// at a time: a half is loaded into it as soon as the one before has left, the warps exchange it for theirs, and theirs
+// goes out.  The next item's first half is there long before its use.  Each round: (load or not) -> st_full -> the
+// exchange -> st_done -> (store or not).  By the state's own threads, row by row, reading and writing a state took
+// 14,000 cycles of an item.
+template <int D, int PARTS, bool STATE_ONLY>
+__device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
+  uint32_t round[2] = {0, 0};
+  bool ok = true;
+  // half of a state as its tensor map's boxes: 32 columns by D rows, or (transposed) by D / 2 rows
+  auto load = [&](const Item& it, int half, bool in, bool swap) {
+    if (!in) {
+      tc::mbar_arrive(&sm.st_full[half]);
+      return;
+    }
+    const CUtensorMap* m = it.nseg > 1 ? &maps.ws : &maps.s_in[it.w];
+    const int row = (it.nseg > 1 ? stretch_index(t, it) : it.n * t.a.H + it.h) * D;
+    mbar_arrive_expect_tx(&sm.st_full[half], LinSmem<D>::STATE);
+    const int boxes = swap ? D / 32 : D / 64, bytes = swap ? D * 64 : D * 128;
+    for (int b = 0; b < boxes; ++b)
+      ltc::tensor_load_2d(smem_addr(sm.st) + b * bytes, m, 32 * b + (swap ? 0 : D / 2 * half), row + (swap ? D / 2 * half : 0),
+                          &sm.st_full[half]);
+  };
+  auto done = [&](const Item& it, int half, bool out, bool swap) {
+    if (!ltc::wait_tries(&sm.st_done[half], round[half]++ & 1u)) return false;
+    if (out) {
+      const CUtensorMap* m = STATE_ONLY ? &maps.ws : &maps.s_out[it.w];
+      const int row = (STATE_ONLY ? stretch_index(t, it) : it.n * t.a.H + it.h) * D;
+      const int boxes = swap ? D / 32 : D / 64, bytes = swap ? D * 64 : D * 128;
+      for (int b = 0; b < boxes; ++b)
+        ltc::tensor_store_2d(m, smem_addr(sm.st) + b * bytes, 32 * b + (swap ? 0 : D / 2 * half), row + (swap ? D / 2 * half : 0));
+      tc::bulk_commit_group();
+      tc::bulk_wait_read_all();
+    }
+    return true;
+  };
+  Item last;
+  StateIo last_io = {false, false, false, false};
+  for (int i = 0; i < item_rounds(t) && ok; ++i) {
+    const Item it = item_of<STATE_ONLY>(t, sm.order, i);
+    if (!it.on) continue;
+    const StateIo io = state_io<STATE_ONLY>(t, it);
+    const bool two = two_rounds(last_io, io);
+    for (int half = 0; half < 2 && ok; ++half) {
+      if (two) {
+        load(last, half, false, false);
+        ok = done(last, half, true, last_io.out_swap);
+        if (!ok) break;
+      }
+      load(it, half, io.in, io.in_swap);
+      ok = done(last, half, !two && last_io.out, last_io.out_swap);
+    }
+    last = it;
+    last_io = io;
+  }
+  for (int half = 0; half < 2 && ok && last_io.out; ++half) {
+    load(last, half, false, false);
+    ok = done(last, half, true, last_io.out_swap);
+  }
+  if (!ok) {
+    gave_up(t.a.flags);
+    // nothing of ours may land after the block has left: a round that gave up had its load before it
+    for (int half = 0; half < 2; ++half)
+      if (round[half]) ltc::wait_tries(&sm.st_full[half], (round[half] - 1) & 1u);
+  }
+  tc::bulk_wait_all();
+}
+
 // ---- products --------------------------------------------------------------------
 // For each chunk U, then OI, then OP: U's loop (the value's parts into TMEM, U, the parts free again) is the longest of
 // the loops over chunks, and OI waits for the state that comes from the last U.  SC of the next chunk goes as soon as P
 // has been made of this one's.
-template <int D, bool STATE_ONLY>
+template <int D, int PARTS, bool STATE_ONLY>
 __device__ void mma_role(const LinTc& t, LinSmem<D>& sm) {
   using SM = LinSmem<D>;
   constexpr uint32_t id_sc = ltc::idesc_bf16(C, C, 0, 0), id_oi = ltc::idesc_bf16(128, C, 0, 0);
@@ -169,7 +303,7 @@ __device__ void mma_role(const LinTc& t, LinSmem<D>& sm) {
   constexpr uint32_t kStage = 3 * SM::TILE / 16;
   // this CTA's chunks, over all its items
   int total = 0;
-  for (int x = blockIdx.x; x < t.items; x += gridDim.x) total += item_of<STATE_ONLY>(t, x).chunks();
+  for (int i = 0; i < item_rounds(t); ++i) total += item_of<STATE_ONLY>(t, sm.order, i).chunks();
   auto scores = [&](int s) {
     if (ltc::elect_one()) {
 #pragma unroll 1
@@ -198,7 +332,7 @@ __device__ void mma_role(const LinTc& t, LinSmem<D>& sm) {
     tc::fence_after_sync();
     if (ltc::elect_one()) {
 #pragma unroll 1
-      for (int part = 0; part < 3; ++part)
+      for (int part = 0; part < PARTS; ++part)
 #pragma unroll
         for (int ks = 0; ks < C / 16; ++ks)
           ltc::mma_ts(T_U, T_V + 32u * part + 8u * ks, kt0 + (kStage * s + 128u * ks), id_u, part + ks > 0);
@@ -290,7 +424,9 @@ __device__ __forceinline__ void make_p(uint32_t p_smem, const float* pz, int sgn
 // Tokens 32 th .. + 31 of the value tile, times their decay, transposed for TMEM lanes 32 qd .. + 31 (channels), two
 // tokens a word, in three bf16 parts.  The parts are cut off, not rounded: 8 bits each of the product's 24, so that
 // their sum is the product.  v[part][16 channels of h][..]: words of token groups 0..3, channels g and g + 8.
-__device__ __forceinline__ void value_parts(uint32_t (&v)[3][2][8], uint32_t tile, const float* wv, int r, int th, int qd, int lane) {
+template <int PARTS>
+__device__ __forceinline__ void value_parts(uint32_t (&v)[PARTS][2][8], uint32_t tile, const float* wv, int r, int th, int qd,
+                                            int lane) {
   const int q = lane & 3;
   // lane's row address of an ldmatrix: matrix lane / 8 = (channels + 8 (m & 1), tokens + 8 (m >> 1)), row lane % 8
   const int m = lane >> 3, tt = lane & 7;
@@ -318,17 +454,17 @@ __device__ __forceinline__ void value_parts(uint32_t (&v)[3][2][8], uint32_t til
     for (int h = 0; h < 2; ++h) {
       float2 p = __fmul2_rn(make_float2(ltc::bf16_lo(v[0][h][x]), ltc::bf16_hi(v[0][h][x])), w);
 #pragma unroll
-      for (int part = 0; part < 3; ++part) {
+      for (int part = 0; part < PARTS; ++part) {
         const uint32_t a0 = __float_as_uint(p.x), a1 = __float_as_uint(p.y);
         v[part][h][x] = ltc::upper_halves(a0, a1);
-        if (part < 2)
+        if (part + 1 < PARTS)
           p = __ffma2_rn(make_float2(__uint_as_float(a0 & 0xffff0000u), __uint_as_float(a1 & 0xffff0000u)), minus, p);
       }
     }
   }
   // made here, not behind the wait that follows
 #pragma unroll
-  for (int part = 0; part < 3; ++part)
+  for (int part = 0; part < PARTS; ++part)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -343,8 +479,8 @@ __device__ __forceinline__ void write_out(const LinTc& t, const LinMaps& maps, L
   tc::fence_after_sync();
   if (32 * qd < D) {
     const int q = lane & 3;
-    uint8_t* os = sm.o[k & 1] + qd * (C * 64);
-    if (lane == 0) ltc::bulk_wait_read_1();      // the store of the tile before the last has left this buffer
+    uint8_t* os = sm.o + qd * (C * 64);
+    if (lane == 0) tc::bulk_wait_read_all();     // the store of the last tile has left this buffer
     __syncwarp();
 #pragma unroll 1
     for (int x = 0; x < 4; ++x) {                // 16 channels, 32 tokens: two each of four blocks, channels g and g + 8
@@ -395,14 +531,14 @@ __device__ __forceinline__ void write_out(const LinTc& t, const LinMaps& maps, L
 
 // Warps 4-7 (th = 0) and 8-11 (th = 1): half of the tokens' value parts each.  They are made while U of the chunk before
 // runs and stored when it is done.
-template <int D, bool STATE_ONLY>
+template <int D, int PARTS, bool STATE_ONLY>
 __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   const int qd = warp & 3, th = (warp - 4) >> 2, tid = 32 * qd + lane;
   int k = 0, n_item = 0, s = 0;
   uint32_t turn = 0;                             // parity of stage s
   bool ok = true;
-  for (int x = blockIdx.x; x < t.items; x += gridDim.x) {
-    const Item it = item_of<STATE_ONLY>(t, x);
+  for (int i = 0; i < item_rounds(t); ++i) {
+    const Item it = item_of<STATE_ONLY>(t, sm.order, i);
     if (it.chunks() == 0) continue;
     const bool back = t.a.walk[it.w].back;
     float(*wv)[C] = sm.wv[n_item & 1][th];
@@ -417,8 +553,8 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int r = it.rows(chunk_at(it, back, c));
       if (!(ok = wait_all(&sm.full[s], turn))) break;
-      uint32_t v[3][2][8];
-      if (32 * qd < D) value_parts(v, smem_addr(sm.stage[s][2]), wv[r < C], r, th, qd, lane);
+      uint32_t v[PARTS][2][8];
+      if (32 * qd < D) value_parts<PARTS>(v, smem_addr(sm.stage[s][2]), wv[r < C], r, th, qd, lane);
       if (r < C) {
         // keys and values behind the sequence's end: zeros, for products of theirs with zeros must be zero
         for (int y = tid; y < (C - r) * (D / 8); y += 128) {
@@ -432,10 +568,11 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       tc::fence_after_sync();
       if (32 * qd < D) {
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
+        for (int part = 0; part < PARTS; ++part) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             ltc::st_16x128b_x4(((uint32_t)(32 * qd + 16 * h) << 16) + T_V + 32u * part + 16u * th, v[part][h]);
+        }
         ltc::wait_st();
       }
       tc::fence_before_sync();
@@ -459,8 +596,8 @@ __device__ void score_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   const int qd = warp & 3, tid = 32 * qd + lane;
   int k = 0, n_item = 0;
   bool ok = true;
-  for (int x = blockIdx.x; x < t.items; x += gridDim.x) {
-    const Item it = item_of<false>(t, x);
+  for (int i = 0; i < item_rounds(t); ++i) {
+    const Item it = item_of<false>(t, sm.order, i);
     if (it.chunks() == 0) continue;
     const bool back = t.a.walk[it.w].back;
     float* pz = sm.pz[n_item & 1];
@@ -488,8 +625,8 @@ __device__ void out_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, in
   const int qd = warp & 3, tid = 32 * qd + lane;
   int k = 0, n_item = 0;
   bool ok = true;
-  for (int x = blockIdx.x; x < t.items; x += gridDim.x) {
-    const Item it = item_of<false>(t, x);
+  for (int i = 0; i < item_rounds(t); ++i) {
+    const Item it = item_of<false>(t, sm.order, i);
     if (it.chunks() == 0) continue;
     const bool back = t.a.walk[it.w].back;
     float(*wo)[C] = sm.wo[n_item & 1];
@@ -523,38 +660,70 @@ __device__ __forceinline__ void state_to_tmem(const float (&S)[D / 2], uint32_t 
   ltc::wait_st();
 }
 
-template <int D, bool STATE_ONLY>
+// This thread's part of the state (row e of its half of the key channels) out of shared memory, into it, or exchanged.  Rows of 128
+// bytes whose 16-byte pieces are exchanged by the row's low bits: the lanes of a row-wise access fall in distinct banks,
+// as those of a column-wise one (`swap`: the state lies transposed) do anyway.
+template <int D>
+__device__ __forceinline__ void exchange_state(float (&S)[D / 2], uint8_t* st, int e, bool swap, bool get, bool put) {
+  constexpr int HC = D / 2;
+  if (!swap) {
+    uint8_t* row = st + e * 128;
+#pragma unroll
+    for (int j = 0; j < HC; j += 4) {
+      float4* at = reinterpret_cast<float4*>(row + (j / 32) * (D * 128) + ((((j % 32) / 4) ^ (e & 7)) << 4));
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (get) x = *at;
+      if (put) *at = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      if (get || put) S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
+    }
+  } else {
+    uint8_t* col = st + (e >> 5) * (D * 64) + (e & 3) * 4;
+    const int piece = (e & 31) >> 2;
+#pragma unroll
+    for (int j = 0; j < HC; ++j) {
+      float* at = reinterpret_cast<float*>(col + j * 128 + ((piece ^ (j & 7)) << 4));
+      float x = 0.f;
+      if (get) x = *at;
+      if (put) *at = S[j];
+      if (get || put) S[j] = x;
+    }
+  }
+}
+
+template <int D, int PARTS, bool STATE_ONLY>
 __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   constexpr int HC = D / 2;                                  // key channels of a thread
   const int qd = warp & 3, half = (warp - 20) >> 2, e = 32 * qd + lane;
   const bool mine = 32 * qd < D;                             // lanes beyond d hold nothing
   const uint32_t lane_addr = (uint32_t)(32 * qd) << 16;
   int k = 0;
+  uint32_t round = 0;
   bool ok = true;
   float S[HC];
-  for (int x = blockIdx.x; x < t.items && ok; x += gridDim.x) {
-    const Item it = item_of<STATE_ONLY>(t, x);
+  StateIo last_io = {false, false, false, false};
+  auto exchange = [&](bool swap, bool get, bool put) {
+    if (!wait_all(&sm.st_full[half], round++ & 1u)) return false;
+    if (mine) exchange_state<D>(S, sm.st, e, swap, get, put);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&sm.st_done[half]);
+    return true;
+  };
+  for (int i = 0; i < item_rounds(t); ++i) {
+    const Item it = item_of<STATE_ONLY>(t, sm.order, i);
     if (!it.on) continue;
-    const LinWalk& w = t.a.walk[it.w];
-    const bool back = w.back;
-    const size_t st0 = ((size_t)it.n * t.a.H + it.h) * D * D;
-    const float* in = STATE_ONLY ? nullptr : (it.nseg > 1 ? stretch_state(t, it) : (w.S_in ? w.S_in + st0 : nullptr));
-    const bool in_swap = it.nseg > 1 ? false : w.swap != 0;
-    float* out = STATE_ONLY ? stretch_state(t, it)
-                            : (w.S_out && it.seg == (back ? 0 : it.nseg - 1) ? w.S_out + st0 : nullptr);
-    const bool out_swap = !STATE_ONLY && w.swap != 0;
-    if (mine) {
-      if (in && in_swap) {
+    const StateIo io = state_io<STATE_ONLY>(t, it);
+    const bool back = t.a.walk[it.w].back;
+    if (two_rounds(last_io, io)) {
+      if (!(ok = exchange(last_io.out_swap, false, true))) break;
+      if (!(ok = exchange(io.in_swap, true, false))) break;
+    } else if (!(ok = exchange(io.in ? io.in_swap : last_io.out_swap, io.in, last_io.out))) {
+      break;
+    }
+    last_io = io;
+    if (!io.in) {
 #pragma unroll
-        for (int j = 0; j < HC; ++j) S[j] = in[(size_t)(HC * half + j) * D + e];
-      } else if (in) {
-#pragma unroll
-        for (int j = 0; j < HC; j += 4)
-          *reinterpret_cast<float4*>(&S[j]) = *reinterpret_cast<const float4*>(in + (size_t)e * D + HC * half + j);
-      } else {
-#pragma unroll
-        for (int j = 0; j < HC; ++j) S[j] = 0.f;
-      }
+      for (int j = 0; j < HC; ++j) S[j] = 0.f;
     }
     // A^rows - 1: S + (A^rows - 1) S keeps what a product with A^rows, rounded to 24 bits, would lose chunk after chunk
     const float g = clamp_log_decay(t.a.log_decay[it.h]);
@@ -615,21 +784,13 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
         if (lane == 0) tc::mbar_arrive(&sm.s_full);
       }
     }
-    if (out && mine && ok) {
-      if (out_swap) {
-#pragma unroll
-        for (int j = 0; j < HC; ++j) out[(size_t)(HC * half + j) * D + e] = S[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < HC; j += 4)
-          *reinterpret_cast<float4*>(out + (size_t)e * D + HC * half + j) = *reinterpret_cast<const float4*>(&S[j]);
-      }
-    }
+    if (!ok) break;
   }
+  if (ok && last_io.out) ok = exchange(last_io.out_swap, false, true);
   if (!ok) gave_up(t.a.flags);
 }
 
-template <int D, bool STATE_ONLY>
+template <int D, int PARTS, bool STATE_ONLY>
 __global__ void __launch_bounds__(kTcThreads, 1)
     linattn_tc_kernel(const __grid_constant__ LinTc t, const __grid_constant__ LinMaps maps) {
   using SM = LinSmem<D>;
@@ -649,33 +810,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&sm.u_empty, 8);
     mbar_init(&sm.op_full, 1);
     mbar_init(&sm.o_empty, 4);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sm.st_full[h], 1);
+      mbar_init(&sm.st_done[h], 4);
+    }
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(&sm.taddr, 512);
+  order_sequences<D>(t, sm);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  // registers: 896 threads x 72 at launch hold 128 x (40 + 72 + 72 + 48 + 56 + 104 + 104)
+  // registers: 896 threads x 72 at launch hold 128 x (40 + 80 + 80 + 48 + 48 + 104 + 104)
   if (warp < 4) {
     ltc::regs_down<40>();
     if (warp == 0) {
-      if (lane == 0) load_role<D, STATE_ONLY>(t, maps, sm);
+      if (lane == 0) load_role<D, PARTS, STATE_ONLY>(t, maps, sm);
       __syncwarp();
     } else if (warp == 1) {
-      mma_role<D, STATE_ONLY>(t, sm);
+      mma_role<D, PARTS, STATE_ONLY>(t, sm);
+    } else if (warp == 2) {
+      if (lane == 0) state_io_role<D, PARTS, STATE_ONLY>(t, maps, sm);
+      __syncwarp();
     }
   } else if (warp < 12) {
-    value_role<D, STATE_ONLY>(t, sm, warp, lane);
+    ltc::regs_up<80>();
+    value_role<D, PARTS, STATE_ONLY>(t, sm, warp, lane);
   } else if (warp < 16) {
     ltc::regs_down<48>();
     if (!STATE_ONLY) score_role<D>(t, sm, warp, lane);
   } else if (warp < 20) {
-    ltc::regs_down<56>();
+    ltc::regs_down<48>();
     if (!STATE_ONLY) out_role<D>(t, maps, sm, warp, lane);
   } else {
     ltc::regs_up<104>();
-    state_role<D, STATE_ONLY>(t, sm, warp, lane);
+    state_role<D, PARTS, STATE_ONLY>(t, sm, warp, lane);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -765,23 +935,38 @@ bool make_map(CUtensorMap* m, const void* p, int64_t width, int64_t stride, int6
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+// states: `count` of D rows of D fp32, in boxes of 32 columns by D rows, or (transposed) by D / 2
+bool make_state_map(CUtensorMap* m, const void* p, int D, int64_t count, bool swap) {
+  EncodeFn encode = encode_fn();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)(count * D)};
+  const cuuint64_t strides[1] = {(cuuint64_t)D * 4};
+  const cuuint32_t box[2] = {32, (cuuint32_t)(swap ? D / 2 : D)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(p), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int PARTS>
 cudaError_t launch_tc(const LinTc& t0, const LinMaps& maps, cudaStream_t st) {
   LinTc t = t0;
   const size_t smem = sizeof(LinSmem<D>) + 1024;
   static_assert(sizeof(LinSmem<D>) + 1024 <= 232448, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<D, PARTS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = (unsigned)(t.items < kSms ? t.items : kSms);
+  // as many blocks for each walk
+  const int64_t all = (int64_t)t.items * t.a.walks;
+  const unsigned blocks = (unsigned)(all < kSms ? all : kSms / t.a.walks * t.a.walks);
   if (t.split.stretches > 1) {
-    e = cudaFuncSetAttribute(linattn_tc_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(linattn_tc_kernel<D, PARTS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    linattn_tc_kernel<D, true><<<blocks, kTcThreads, smem, st>>>(t, maps);
+    linattn_tc_kernel<D, PARTS, true><<<blocks, kTcThreads, smem, st>>>(t, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     linattn_chain_kernel<D><<<dim3((unsigned)(t.a.N * t.a.H * t.a.walks), D == 128 ? 4 : 1), 256, 0, st>>>(t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  linattn_tc_kernel<D, false><<<blocks, kTcThreads, smem, st>>>(t, maps);
+  linattn_tc_kernel<D, PARTS, false><<<blocks, kTcThreads, smem, st>>>(t, maps);
   return cudaGetLastError();
 }
 
@@ -804,6 +989,8 @@ LinSplit linattn_tc_split(int64_t heads, int64_t max_len, int walks) {
 
 bool linattn_tc_takes(const LinArgs& a) {
   if (a.io != PACE_IO_BF16 || (a.D != 64 && a.D != 128) || a.total == 0) return false;
+  // rows of the states, as a tensor load's coordinate
+  if ((int64_t)a.N * a.H * a.D > 0x7fffffffll) return false;
   for (int w = 0; w < a.walks; ++w) {
     const LinWalk& k = a.walk[w];
     if (((uintptr_t)k.query | (uintptr_t)k.key | (uintptr_t)k.value | (uintptr_t)k.out) % 16) return false;
@@ -818,8 +1005,8 @@ cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, c
   t.a = a;
   t.split = sp;
   t.ws = ws;
-  const int64_t items = (int64_t)a.N * a.H * a.walks * sp.stretches;
-  if (items > 0x7fffffffll) return cudaErrorInvalidValue;
+  const int64_t items = (int64_t)a.N * a.H * sp.stretches;
+  if (items * a.walks > 0x7fff0000ll) return cudaErrorInvalidValue;
   t.items = (int32_t)items;
   // the tensors of all walks, each mapped once
   struct Seen { const void* p; int64_t stride; } seen[4];
@@ -838,7 +1025,15 @@ cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, c
     if (t.map_q[w] < 0 || t.map_k[w] < 0 || t.map_v[w] < 0) return cudaErrorInvalidValue;
     if (!make_map(&maps.out[w], a.walk[w].out, (int64_t)a.H * a.D, a.walk[w].out_stride, a.total, 32)) return cudaErrorInvalidValue;
   }
-  return a.D == 128 ? launch_tc<128>(t, maps, st) : launch_tc<64>(t, maps, st);
+  for (int w = 0; w < a.walks; ++w) {
+    if (a.walk[w].S_in && !make_state_map(&maps.s_in[w], a.walk[w].S_in, a.D, (int64_t)a.N * a.H, a.walk[w].swap)) return cudaErrorInvalidValue;
+    if (a.walk[w].S_out && !make_state_map(&maps.s_out[w], a.walk[w].S_out, a.D, (int64_t)a.N * a.H, a.walk[w].swap)) return cudaErrorInvalidValue;
+  }
+  if (sp.stretches > 1 && !make_state_map(&maps.ws, ws, a.D, items * a.walks, false)) return cudaErrorInvalidValue;
+  // gradients without dS0 are bf16 all; the forward operator's outputs do not depend on whether ST is wanted
+  const bool two = a.walks > 1 && !a.walk[0].S_out && !a.walk[1].S_out && !a.walk[2].S_out;
+  if (two) return a.D == 128 ? launch_tc<128, 2>(t, maps, st) : launch_tc<64, 2>(t, maps, st);
+  return a.D == 128 ? launch_tc<128, 3>(t, maps, st) : launch_tc<64, 3>(t, maps, st);
 }
 
 }  // namespace pace
