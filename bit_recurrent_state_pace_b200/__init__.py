@@ -432,13 +432,24 @@ class _On:
         return False
 
 
+def _run(name: str, fn, index: int, stream, *args) -> None:
+    """fn(*args, stream) with device `index` current."""
+    if stream is None and _raw_stream is not None and torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with _On(index, stream) as st:
+            status = fn(*args, st)
+    if status != PACE_OK:
+        raise PaceError(name, status)
+
+
 # What a call's shapes, strides, types and devices lead to (the checks passed, the descriptor, sizes), kept so that
 # the next call of the same form pays for a lookup; no tensor and no address is kept.
 _plans: dict = {}
 
 
 def _form(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
 def _plan(key, build):
@@ -462,6 +473,13 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), like.device)
     with torch.cuda.stream(s):
         return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """A packed tensor of t's shape and type for work on `stream`."""
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _new(t.shape, t.dtype, t, stream)
 
 
 def _workspace(name: str, nbytes: int, given: Optional[torch.Tensor], like: torch.Tensor, stream):
@@ -525,10 +543,10 @@ def pace_linattn_forward(q, k, v, log_decay, o=None, ST=None, num_seqs=None, max
     cu_seqlens: int32 [N + 1], or None for prompts of one length; S0, ST: fp32 [N, H, d, d].  Rows of no sequence
     are left as they are (unset in an o made here).
     """
-    _tensors(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("o", o), ("ST", ST), ("cu_seqlens", cu_seqlens),
-             ("S0", S0), ("flags", flags))
 
     def build():
+        _tensors(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("o", o), ("ST", ST), ("cu_seqlens", cu_seqlens),
+                 ("S0", S0), ("flags", flags))
         desc, total, n, H, d = _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens)
         if o is not None:
             to, desc.o_stride = _rows("o", o, H, d, q)
@@ -543,14 +561,12 @@ def pace_linattn_forward(q, k, v, log_decay, o=None, ST=None, num_seqs=None, max
     desc, ref, states, size = _plan(("fwd", _form(q), _form(k), _form(v), _form(log_decay), _form(o), _form(ST),
                                      _form(cu_seqlens), _form(S0), _form(flags), num_seqs, max_len), build)
     if o is None:
-        o = _new(q.shape, q.dtype, q, stream)
+        o = _like(q, stream)
     if ST is None and need_ST:
-        ST = _new(states, torch.float32, q, stream)
+        ST = _new(states, torch.float32, q, stream) if S0 is None else _like(S0, stream)
     ws = _workspace("pace_linattn_forward", size, workspace, q, stream)
-    with _On(q.device.index, stream) as s:
-        _check("pace_linattn_forward", lib.pace_linattn_forward(
-            ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _opt(cu_seqlens), _opt(S0), o.data_ptr(),
-            _opt(ST), _opt(ws), _opt(flags), s))
+    _run("pace_linattn_forward", lib.pace_linattn_forward, q.device.index, stream, ref, q.data_ptr(), k.data_ptr(),
+         v.data_ptr(), log_decay.data_ptr(), _opt(cu_seqlens), _opt(S0), o.data_ptr(), _opt(ST), _opt(ws), _opt(flags))
     return o, ST
 
 
@@ -560,10 +576,10 @@ def pace_linattn_backward(q, k, v, log_decay, d_o, dq=None, dk=None, dv=None, dS
 
     dq, dk, dv have the row strides of q, k, v; those not given are made so (rows of no sequence are left unset).
     """
-    _tensors(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("d_o", d_o), ("dq", dq), ("dk", dk), ("dv", dv),
-             ("dS0", dS0), ("cu_seqlens", cu_seqlens), ("S0", S0), ("dST", dST), ("flags", flags))
 
     def build():
+        _tensors(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("d_o", d_o), ("dq", dq), ("dk", dk), ("dv", dv),
+                 ("dS0", dS0), ("cu_seqlens", cu_seqlens), ("S0", S0), ("dST", dST), ("flags", flags))
         desc, total, n, H, d = _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens)
         to, desc.o_stride = _rows("d_o", d_o, H, d, q)
         _need(to == total, "d_o: as many rows as q")
@@ -587,25 +603,24 @@ def pace_linattn_backward(q, k, v, log_decay, d_o, dq=None, dk=None, dv=None, dS
     made = []
     for given, like, room in ((dq, q, rooms[0]), (dk, k, rooms[1]), (dv, v, rooms[2])):
         if given is None:
-            given = (_new(like.shape, like.dtype, q, stream) if room is None
+            given = (_like(like, stream) if room is None
                      else _new(room, like.dtype, q, stream).as_strided(like.shape, like.stride()))
         made.append(given)
     dq, dk, dv = made
     if dS0 is None and (S0 is not None if need_dS0 is None else need_dS0):
         dS0 = _new(states, torch.float32, q, stream)
     ws = _workspace("pace_linattn_backward", size, workspace, q, stream)
-    with _On(q.device.index, stream) as s:
-        _check("pace_linattn_backward", lib.pace_linattn_backward(
-            ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _opt(cu_seqlens), _opt(S0), d_o.data_ptr(),
-            _opt(dST), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _opt(dS0), _opt(ws), _opt(flags), s))
+    _run("pace_linattn_backward", lib.pace_linattn_backward, q.device.index, stream, ref, q.data_ptr(), k.data_ptr(),
+         v.data_ptr(), log_decay.data_ptr(), _opt(cu_seqlens), _opt(S0), d_o.data_ptr(), _opt(dST), dq.data_ptr(),
+         dk.data_ptr(), dv.data_ptr(), _opt(dS0), _opt(ws), _opt(flags))
     return dq, dk, dv, dS0
 
 
 def pace_linattn_step(S, q, k, v, log_decay, o=None, stream=None) -> torch.Tensor:
     """One token for each of N sequences: q, k, v [N, H, d]; S fp32 [N, H, d, d] is updated in place; returns o."""
-    _tensors(("S", S), ("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("o", o))
 
     def build():
+        _tensors(("S", S), ("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("o", o))
         _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q: device tensor [N, H, d]")
         _need(q.dtype in _IO_OF, f"q: bfloat16 or float32, not {q.dtype}")
         n, H, d = q.shape
@@ -622,10 +637,9 @@ def pace_linattn_step(S, q, k, v, log_decay, o=None, stream=None) -> torch.Tenso
 
     _, ref = _plan(("step", _form(S), _form(q), _form(k), _form(v), _form(log_decay), _form(o)), build)
     if o is None:
-        o = _new(q.shape, q.dtype, q, stream)
-    with _On(q.device.index, stream) as s:
-        _check("pace_linattn_step", lib.pace_linattn_step(ref, S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                                          log_decay.data_ptr(), o.data_ptr(), s))
+        o = _like(q, stream)
+    _run("pace_linattn_step", lib.pace_linattn_step, q.device.index, stream, ref, S.data_ptr(), q.data_ptr(), k.data_ptr(),
+         v.data_ptr(), log_decay.data_ptr(), o.data_ptr())
     return o
 
 
@@ -667,10 +681,10 @@ def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_
 
     q: [tokens, Hq, d], k: [tokens, Hk, d] (either may be None); q_out may be q, k_out may be k.
     """
-    _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),
-             ("inv_freq", inv_freq), ("q_out", q_out), ("k_out", k_out))
 
     def build():
+        _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),
+                 ("inv_freq", inv_freq), ("q_out", q_out), ("k_out", k_out))
         desc, like, heads, rows, d = _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved, norm,
                                               eps, q_scale)
         for i, (name, t, x) in enumerate((("q_out", q_out, q), ("k_out", k_out, k))):
@@ -688,12 +702,11 @@ def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_
     _, ref = _plan(("norm", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq),
                     _form(q_out), _form(k_out), rotary_dim, interleaved, norm, eps, q_scale), build)
     if q_out is None and q is not None:
-        q_out = _new(q.shape, q.dtype, q, stream)
+        q_out = _like(q, stream)
     if k_out is None and k is not None:
-        k_out = _new(k.shape, k.dtype, k, stream)
-    with _On((q if q is not None else k).device.index, stream) as s:
-        _check("pace_qk_norm_rotate", lib.pace_qk_norm_rotate(
-            ref, _opt(q), _opt(k), _opt(q_weight), _opt(k_weight), _opt(positions), _opt(inv_freq), _opt(q_out), _opt(k_out), s))
+        k_out = _like(k, stream)
+    _run("pace_qk_norm_rotate", lib.pace_qk_norm_rotate, (k if q is None else q).device.index, stream, ref, _opt(q), _opt(k),
+         _opt(q_weight), _opt(k_weight), _opt(positions), _opt(inv_freq), _opt(q_out), _opt(k_out))
     return q_out, k_out
 
 
@@ -709,11 +722,11 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
                                  q_scale=1.0, workspace=None, stream=None):
     """Gradients of pace_qk_norm_rotate: returns (dq, dk, dq_weight, dk_weight); a weight's gradient is made where the
     weight is given (or a tensor for it)."""
-    _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),
-             ("inv_freq", inv_freq), ("d_q_out", d_q_out), ("d_k_out", d_k_out), ("dq", dq), ("dk", dk),
-             ("dq_weight", dq_weight), ("dk_weight", dk_weight))
 
     def build():
+        _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),
+                 ("inv_freq", inv_freq), ("d_q_out", d_q_out), ("d_k_out", d_k_out), ("dq", dq), ("dk", dk),
+                 ("dq_weight", dq_weight), ("dk_weight", dk_weight))
         desc, like, heads, rows, d = _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved, norm,
                                               eps, q_scale)
         for i, (x, dy, dx, dw) in enumerate(((q, d_q_out, dq, dq_weight), (k, d_k_out, dk, dk_weight))):
@@ -742,9 +755,9 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
          q_scale), build)
     like = q if q is not None else k
     if dq is None and q is not None:
-        dq = _new(q.shape, q.dtype, q, stream)
+        dq = _like(q, stream)
     if dk is None and k is not None:
-        dk = _new(k.shape, k.dtype, k, stream)
+        dk = _like(k, stream)
     if dq_weight is None and q is not None and q_weight is not None:
         dq_weight = _new(wide, torch.float32, like, stream)
     if dk_weight is None and k is not None and k_weight is not None:
@@ -752,10 +765,9 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
     ws = None
     if dq_weight is not None or dk_weight is not None:
         ws = _workspace("pace_qk_norm_rotate_backward", size, workspace, like, stream)
-    with _On(like.device.index, stream) as s:
-        _check("pace_qk_norm_rotate_backward", lib.pace_qk_norm_rotate_backward(
-            ref, _opt(q), _opt(k), _opt(q_weight), _opt(k_weight), _opt(positions), _opt(inv_freq), _opt(d_q_out),
-            _opt(d_k_out), _opt(dq), _opt(dk), _opt(dq_weight), _opt(dk_weight), _opt(ws), s))
+    _run("pace_qk_norm_rotate_backward", lib.pace_qk_norm_rotate_backward, like.device.index, stream, ref, _opt(q), _opt(k),
+         _opt(q_weight), _opt(k_weight), _opt(positions), _opt(inv_freq), _opt(d_q_out), _opt(d_k_out), _opt(dq), _opt(dk),
+         _opt(dq_weight), _opt(dk_weight), _opt(ws))
     return dq, dk, dq_weight, dk_weight
 
 

@@ -55,6 +55,19 @@ __device__ __forceinline__ void seq_rows(const LinArgs& a, int n, int* begin, in
 __device__ __forceinline__ float clamp_log_decay(float g) { return g < -1000.f ? -1000.f : g; }
 __device__ __forceinline__ float decay_pow(float g, int n) { return expf(g * (float)n); }
 
+// Lets `kernel` have `bytes` of dynamic shared memory, on the first call for a device (`done` is the caller's own, one
+// for each kernel; calls at the same time set the same thing).
+template <class K>
+inline cudaError_t allow_shared(K kernel, int bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
 cudaError_t launch_linattn_stream(const LinArgs& a, cudaStream_t st);
 cudaError_t launch_linattn_step(float* S, const void* q, const void* k, const void* v, const float* log_decay, void* o,
                                 int64_t qs, int64_t ks, int64_t vs, int64_t os, int N, int H, int D, int io,

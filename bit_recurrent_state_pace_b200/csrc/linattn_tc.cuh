@@ -69,14 +69,15 @@ __device__ __forceinline__ void st_16x128b_x4(uint32_t taddr, const uint32_t (&r
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// Wait for phase `parity` of `bar`; false after kWaitTries tests.  A test suspends the thread for at most 10 us, so that
-// giving up takes 2 s at most and, should no test suspend, still some milliseconds.  Few instructions: the roles of the
-// kernel share the instruction cache, and a wait with a clock in it cost hundreds of cycles of misses.
+// Wait for phase `parity` of `bar`; false after kWaitTries tests.  The first test is one without a time limit, which
+// costs 52 cycles where the phase is complete (133 with one); a later one suspends the thread for at most 10 us, so that
+// giving up takes 2 s at most and, should no test suspend, still some milliseconds.
 constexpr uint32_t kWaitTries = 200000;
 __device__ __forceinline__ bool wait_tries(uint64_t* bar, uint32_t parity) {
   uint32_t left;
   asm volatile(
       "{\n .reg .pred p, z;\n mov.u32 %0, %3;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE_%=;\n"
       "WAIT_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n @p bra DONE_%=;\n"
       " sub.u32 %0, %0, 1;\n setp.ne.u32 z, %0, 0;\n @z bra WAIT_%=;\nDONE_%=:\n}\n"
       : "=&r"(left)

@@ -23,7 +23,8 @@
 //
 // One persistent CTA of 28 warps per SM, each group of four (a TMEM lane quadrant each) with one job, so that their
 // latencies overlap:
-//  * warp 0: loads the chunks' tiles by TMA, a chunk ahead; warp 1: issues the products; warp 2: the states by TMA;
+//  * warp 0: loads the chunks' tiles by TMA, two chunks ahead; warp 2: the states;
+//  * warp 1 issues U, warp 3 SC, OI and OP: by one warp, every product waited for the slowest of the others' operands;
 //  * warps 4-11: the value's decayed parts into TMEM, half of the tokens each four;
 //  * warps 12-15: P from SC;  warps 16-19: the output, stored by TMA;
 //  * warps 20-27: the state, half of the key channels each four.
@@ -47,7 +48,19 @@ constexpr int kSms = 148;             // B200
 constexpr int kMaxSorted = 512;       // sequences that are put in order (more come out even anyway)
 
 // TMEM columns.  All 512 are allocated, so the allocation begins at column 0.
-constexpr uint32_t T_SC = 0, T_OI = 64, T_OP = 128, T_U = 192, T_S = 320, T_V = 384;
+constexpr uint32_t T_SC = 0, T_OI = 64, T_OP = 128, T_S = 320;
+// U and the value's parts: one buffer each, or two where only states are wanted and there is room
+template <bool STATE_ONLY>
+__device__ __forceinline__ uint32_t t_u(int k) { return STATE_ONLY ? 128u * (k & 1) : 192u; }
+template <bool STATE_ONLY>
+__device__ __forceinline__ uint32_t t_v(int k) { return STATE_ONLY ? 256u + 96u * (k & 1) : 384u; }
+// Chunk k's phase of a barrier kept for each buffer, and whether an earlier chunk had the buffer.
+template <bool STATE_ONLY>
+__device__ __forceinline__ int buffer_of(int k) { return STATE_ONLY ? (k & 1) : 0; }
+template <bool STATE_ONLY>
+__device__ __forceinline__ uint32_t phase_of(int k) { return (uint32_t)((STATE_ONLY ? k >> 1 : k) & 1); }
+template <bool STATE_ONLY>
+__device__ __forceinline__ bool used_before(int k) { return k >= (STATE_ONLY ? 2 : 1); }
 
 struct LinMaps {
   CUtensorMap in[4], out[kLinMaxWalks];              // the packed tensors
@@ -59,7 +72,7 @@ struct LinTc {
   int32_t map_q[kLinMaxWalks], map_k[kLinMaxWalks], map_v[kLinMaxWalks];
   LinSplit split;
   float* ws;               // [walks][N][H][stretches][D][D]: each stretch's state
-  int32_t items;           // of one walk: (n, h, stretch)
+  int32_t items;           // (n, h, stretch, walk)
 };
 
 template <int D>
@@ -69,14 +82,14 @@ struct alignas(1024) LinSmem {
   uint8_t p[2][C * 128];                                 // P[i][j] in two bf16 parts, 128-byte swizzle
   static constexpr int STATE = D * D * 2;                // half of a state (D / 2 key channels)
   uint8_t st[STATE];                                     // states on their way in and out: rows of 128 bytes, swizzled
-  uint8_t o[TILE];                                       // output tile on its way to memory: 64 rows of 32 channels a warp
+  uint8_t o[4][C * 64];                                  // outputs on their way: 64 rows of 32 channels for each lane quadrant
   // tables of the decay, of two items in turn, each group of warps its own:
   float wv[2][2][2][C];                                  // warps 4-7, 8-11: decay of a token's value in the state behind a
                                                          // full chunk, and behind the sequence's last one (zeros beyond it)
   float pz[2][2 * C + 8];                                // warps 12-15: A^n at [C + n], zeros below
   float wo[2][2][C];                                     // warps 16-19: of the state in a token's output, as wv
   uint64_t full[NST], empty[NST];
-  uint64_t sc_full, p_full, v_full, s_full, u_full, u_empty, op_full, o_empty, st_full[2], st_done[2], drain;
+  uint64_t sc_full, sc_empty, p_full, v_full[2], s_full, u_full[2], u_empty[2], op_full, o_empty, st_full[2], st_done[2], drain[2];
   int chunks[kMaxSorted];                                // of each sequence
   uint16_t order[kMaxSorted];                            // sequences, the longest first
   uint32_t taddr;
@@ -99,18 +112,15 @@ struct Item {
 };
 
 // The k-th item of this block (order_sequences says which those are), for k < item_rounds.
-__device__ __forceinline__ int item_rounds(const LinTc& t) {
-  const int groups = gridDim.x / t.a.walks;
-  return (t.items + groups - 1) / groups;
-}
+__device__ __forceinline__ int item_rounds(const LinTc& t) { return (t.items + (int)gridDim.x - 1) / (int)gridDim.x; }
 template <bool STATE_ONLY>
 __device__ __forceinline__ Item item_of(const LinTc& t, const uint16_t* order, int k) {
-  const int groups = gridDim.x / t.a.walks, b = blockIdx.x / t.a.walks;
-  int x = k * groups + ((k & 1) ? groups - 1 - b : b);
+  int x = k * (int)gridDim.x + (int)(t.a.cu && (k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   Item it;
   const bool there = x < t.items;
   if (!there) x = 0;
-  it.w = t.a.walks > 1 ? blockIdx.x % t.a.walks : 0;
+  it.w = x % t.a.walks;
+  x /= t.a.walks;
   it.seg = x % t.split.stretches;
   x /= t.split.stretches;
   it.h = x % t.a.H;
@@ -161,11 +171,12 @@ __device__ __forceinline__ bool two_rounds(const StateIo& last, const StateIo& n
 __device__ __forceinline__ int chunk_at(const Item& it, bool back, int k) { return back ? it.c1 - 1 - k : it.c0 + k; }
 
 // ---- which items a block takes ------------------------------------------------------
-// A walk's items (sequence, head, stretch) are dealt to its blocks in turn, back and forth, the longest sequences first
-// where lengths differ: the heads of a sequence run at the same time, so that their parts of a token's row are read
-// together, and the blocks' sums come out about even.  (Dealt in the order given, 64 prompts of 1 to 1021 tokens kept
-// some blocks busy twice as long as the mean; contiguous shares of equal cost were a fifth slower than that.)  Blocks
-// b, b + 1, b + 2 of a backward pass take the same heads in its three walks, which read the same tensors.
+// The items -- sequence, head, stretch, walk -- are dealt to the blocks in turn: the heads of a sequence run at the same
+// time, so that their parts of a token's row are read together, and so do the three walks of a backward pass over a
+// head, which read the same tensors.  (A block that keeps to one walk took 7 % longer.)  Where lengths differ the longest
+// sequences go first, back and forth, and the blocks' sums come out about even: in the order given, 64 prompts of 1 to
+// 1021 tokens kept some blocks busy twice as long as the mean; contiguous shares of equal cost were a fifth slower than
+// that.
 template <int D>
 __device__ void order_sequences(const LinTc& t, LinSmem<D>& sm) {
   if (!t.a.cu || t.a.N > kMaxSorted) return;
@@ -285,25 +296,64 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
 }
 
 // ---- products --------------------------------------------------------------------
-// For each chunk U, then OI, then OP: U's loop (the value's parts into TMEM, U, the parts free again) is the longest of
-// the loops over chunks, and OI waits for the state that comes from the last U.  SC of the next chunk goes as soon as P
-// has been made of this one's.
+// This CTA's chunks, over all its items.
+template <int D, bool STATE_ONLY>
+__device__ __forceinline__ int chunks_of_block(const LinTc& t, const LinSmem<D>& sm) {
+  int total = 0;
+  for (int i = 0; i < item_rounds(t); ++i) total += item_of<STATE_ONLY>(t, sm.order, i).chunks();
+  return total;
+}
+// every product that the calling warp issued has completed (TMEM is released after that)
+template <int D>
+__device__ __forceinline__ void drain(LinSmem<D>& sm, int which) {
+  if (ltc::elect_one()) tc::commit(&sm.drain[which]);
+  __syncwarp();
+  ltc::wait_tries(&sm.drain[which], 0);
+}
+
+// Warp 1: U of each chunk, as soon as the value's parts are there and the last U has been read.
 template <int D, int PARTS, bool STATE_ONLY>
-__device__ void mma_role(const LinTc& t, LinSmem<D>& sm) {
+__device__ void update_role(const LinTc& t, LinSmem<D>& sm, int total) {
   using SM = LinSmem<D>;
-  constexpr uint32_t id_sc = ltc::idesc_bf16(C, C, 0, 0), id_oi = ltc::idesc_bf16(128, C, 0, 0);
-  constexpr uint32_t id_op = ltc::idesc_bf16(128, C, 1, 0), id_u = ltc::idesc_bf16(128, D, 0, 1);
+  constexpr uint32_t id_u = ltc::idesc_bf16(128, D, 0, 1);
   // descriptors of stage 0; a tile or step further is its bytes / 16 more
+  const uint64_t kt0 = tc::smem_desc(smem_addr(sm.stage[0][1]), C * 128, 1024, tc::kSwizzle128);
+  constexpr uint32_t kStage = 3 * SM::TILE / 16;
+  bool ok = true;
+  int s = 0;
+  for (int k = 0; k < total; ++k) {
+    const int b = buffer_of<STATE_ONLY>(k);
+    const uint32_t par = phase_of<STATE_ONLY>(k);
+    if (!(ok = wait_all(&sm.v_full[b], par))) break;
+    if (used_before<STATE_ONLY>(k) && !(ok = wait_all(&sm.u_empty[b], par ^ 1u))) break;
+    tc::fence_after_sync();
+    if (ltc::elect_one()) {
+#pragma unroll 1
+      for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks)
+          ltc::mma_ts(t_u<STATE_ONLY>(k), t_v<STATE_ONLY>(k) + 32u * part + 8u * ks, kt0 + (kStage * s + 128u * ks), id_u, part + ks > 0);
+      tc::commit(&sm.u_full[b]);
+      tc::commit(&sm.empty[s]);
+    }
+    __syncwarp();
+    s = s + 1 == NST ? 0 : s + 1;
+  }
+  if (!ok) gave_up(t.a.flags);
+  drain<D>(sm, 0);
+}
+
+// Warp 3: SC of the next chunk as soon as this one's has been read, then this one's OI and OP.
+template <int D>
+__device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
+  using SM = LinSmem<D>;
+  constexpr uint32_t id_sc = ltc::idesc_bf16(C, C, 0, 0), id_oi = ltc::idesc_bf16(128, C, 0, 0), id_op = ltc::idesc_bf16(128, C, 1, 0);
   const uint64_t q0 = tc::smem_desc(smem_addr(sm.stage[0][0]), 16, 1024, tc::kSwizzle128);
   const uint64_t k0 = tc::smem_desc(smem_addr(sm.stage[0][1]), 16, 1024, tc::kSwizzle128);
-  const uint64_t kt0 = tc::smem_desc(smem_addr(sm.stage[0][1]), C * 128, 1024, tc::kSwizzle128);
   // the value as A has 128 rows; for d = 64 its one block of channels twice, the upper lanes are not read
   const uint64_t vt0 = tc::smem_desc(smem_addr(sm.stage[0][2]), D == 128 ? C * 128 : 0, 1024, tc::kSwizzle128);
   const uint64_t p0 = tc::smem_desc(smem_addr(sm.p), 16, 1024, tc::kSwizzle128);
   constexpr uint32_t kStage = 3 * SM::TILE / 16;
-  // this CTA's chunks, over all its items
-  int total = 0;
-  for (int i = 0; i < item_rounds(t); ++i) total += item_of<STATE_ONLY>(t, sm.order, i).chunks();
   auto scores = [&](int s) {
     if (ltc::elect_one()) {
 #pragma unroll 1
@@ -319,7 +369,7 @@ __device__ void mma_role(const LinTc& t, LinSmem<D>& sm) {
     __syncwarp();
   };
   bool ok = true;
-  if (!STATE_ONLY && total > 0) {
+  if (total > 0) {
     ok = wait_all(&sm.full[0], 0);
     if (ok) scores(0);
   }
@@ -327,97 +377,77 @@ __device__ void mma_role(const LinTc& t, LinSmem<D>& sm) {
   for (int k = 0; k < total && ok; ++k) {
     const uint32_t par = (uint32_t)(k & 1);
     const int sn = s + 1 == NST ? 0 : s + 1, turn_n = s + 1 == NST ? turn + 1 : turn;
-    if (!(ok = wait_all(&sm.v_full, par))) break;
-    if (k > 0 && !(ok = wait_all(&sm.u_empty, par ^ 1u))) break;
+    if (k + 1 < total) {
+      if (!(ok = wait_all(&sm.sc_empty, par))) break;
+      if (!(ok = wait_all(&sm.full[sn], (uint32_t)(turn_n & 1)))) break;
+      tc::fence_after_sync();
+      scores(sn);
+    }
+    // the state before the chunk is in TMEM, and the last chunk's output has been read
+    if (!(ok = wait_all(&sm.s_full, par))) break;
+    if (k > 0 && !(ok = wait_all(&sm.o_empty, par ^ 1u))) break;
     tc::fence_after_sync();
     if (ltc::elect_one()) {
 #pragma unroll 1
-      for (int part = 0; part < PARTS; ++part)
+      for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-        for (int ks = 0; ks < C / 16; ++ks)
-          ltc::mma_ts(T_U, T_V + 32u * part + 8u * ks, kt0 + (kStage * s + 128u * ks), id_u, part + ks > 0);
-      tc::commit(&sm.u_full);
-      if (STATE_ONLY) tc::commit(&sm.empty[s]);
+        for (int ks = 0; ks < 4; ++ks)
+          ltc::mma_ts(T_OI, T_S + 32u * b + 8u * ks, q0 + (kStage * s + b * (C * 8) + ks * 2u), id_oi, b + ks > 0);
     }
     __syncwarp();
-    if (!STATE_ONLY) {
-      if (!(ok = wait_all(&sm.p_full, par))) break;
-      if (k + 1 < total) {
-        if (!(ok = wait_all(&sm.full[sn], (uint32_t)(turn_n & 1)))) break;
-        tc::fence_after_sync();
-        scores(sn);
-      }
-      // the state before the chunk is in TMEM, and the last chunk's output has been read
-      if (!(ok = wait_all(&sm.s_full, par))) break;
-      if (k > 0 && !(ok = wait_all(&sm.o_empty, par ^ 1u))) break;
-      tc::fence_after_sync();
-      if (ltc::elect_one()) {
+    // P of this chunk, and zeros in its values behind the sequence's end
+    if (!(ok = wait_all(&sm.p_full, par))) break;
+    tc::fence_after_sync();
+    if (ltc::elect_one()) {
 #pragma unroll 1
-        for (int b = 0; b < D / 64; ++b)
+      for (int b = 0; b < 2; ++b)            // the parts of P one behind the other
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            ltc::mma_ts(T_OI, T_S + 32u * b + 8u * ks, q0 + (kStage * s + b * (C * 8) + ks * 2u), id_oi, b + ks > 0);
-#pragma unroll
-        for (int ks = 0; ks < 2 * (C / 16); ++ks)          // the parts of P one behind the other
-          tc::mma_f16(T_OP, vt0 + (kStage * s + 128u * (ks & 3)), p0 + (ks >> 2) * (C * 8) + 2u * (ks & 3), id_op, ks > 0);
-        tc::commit(&sm.op_full);
-        tc::commit(&sm.empty[s]);
-      }
-      __syncwarp();
+        for (int ks = 0; ks < C / 16; ++ks)
+          tc::mma_f16(T_OP, vt0 + (kStage * s + 128u * ks), p0 + b * (C * 8) + 2u * ks, id_op, b + ks > 0);
+      tc::commit(&sm.op_full);
+      tc::commit(&sm.empty[s]);
     }
+    __syncwarp();
     s = sn;
     turn = turn_n;
   }
   if (!ok) gave_up(t.a.flags);
-  // every product issued has completed before TMEM is released
-  if (ltc::elect_one()) tc::commit(&sm.drain);
-  __syncwarp();
-  ltc::wait_tries(&sm.drain, 0);
+  drain<D>(sm, 1);
 }
 
 // ---- P, the value's parts, the output -------------------------------------------------
-// These run in short loops on purpose: unrolled, the roles' code was 73 KB and every wait and every step began with
-// instruction cache misses, about 300 cycles each.
-
-// Rows 16 qd .. + 15 of P, from the scores on 16 TMEM lanes of this warp's quadrant.  pz: &sm.pz[..][C], A^n at [n] and
-// zeros below; sgn: 1 forwards, -1 backwards.
-__device__ __forceinline__ void make_p(uint32_t p_smem, const float* pz, int sgn, int r, int qd, int lane) {
+// Rows 16 qd .. + 15 of P from the scores x (this warp's 16 TMEM lanes as 16x256b fragments): times their decay, in two
+// bf16 parts, x[2 c + ..] the upper ones of column block c (rows g, g + 8) and x[16 + 2 c + ..] the rest.  pz:
+// &sm.pz[..][C], A^n at [n] and zeros below; sgn: 1 forwards, -1 backwards.
+__device__ __forceinline__ void make_p(uint32_t (&x)[32], const float* pz, int sgn, int r, int qd, int lane) {
   const int g = lane >> 2, q = lane & 3;
+  if (r < C) {                                   // scores of keys behind the sequence's end may be anything
+#pragma unroll
+    for (int y = 0; y < 32; ++y)
+      if (8 * (y >> 2) + 2 * q + (y & 1) >= r) x[y] = 0u;
+  }
   // age of (row 16 qd + g, column 8 c + 2 q): sgn (base - 8 c); the next column's is sgn less, and the row 8 below has
   // the age of the column block before
   const float* at = pz + sgn * (16 * qd + g - 2 * q + 8);
-  const uint32_t row = 16 * qd + (lane & 15);    // stmatrix: the row whose address this lane gives
   float2 w0 = make_float2(at[0], at[-sgn]);
-  auto split = [](float2 x, uint32_t* hi, uint32_t* lo) {
-    *hi = ltc::pack_bf16(x.x, x.y);
-    *lo = ltc::pack_bf16(x.x - ltc::bf16_lo(*hi), x.y - ltc::bf16_hi(*hi));
+  uint32_t hi[16], lo[16];
+  auto split = [](float2 v, uint32_t* h, uint32_t* l) {
+    *h = ltc::pack_bf16(v.x, v.y);
+    *l = ltc::pack_bf16(v.x - ltc::bf16_lo(*h), v.y - ltc::bf16_hi(*h));
   };
-#pragma unroll 1
-  for (int c = 0; c < 8; c += 2) {
-    uint32_t sc[8], m[4], l[4];
-    ltc::ld_16x256b_x2(((uint32_t)(32 * qd) << 16) + T_SC + 8 * c, sc);
-    const float2 w1 = make_float2(at[-8 * sgn], at[-9 * sgn]), w2 = make_float2(at[-16 * sgn], at[-17 * sgn]);
-    at -= 16 * sgn;
-    tc::wait_ld();
-    if (r < C) {                                 // scores of keys behind the sequence's end may be anything
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (8 * (c + (x >> 2)) + 2 * q + (x & 1) >= r) sc[x] = 0u;
-    }
-    const float2 w[3] = {w0, w1, w2};
+  for (int c = 0; c < 8; ++c) {
+    at -= 8 * sgn;
+    const float2 w1 = make_float2(at[0], at[-sgn]);
+    split(__fmul2_rn(make_float2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), w1), &hi[2 * c], &lo[2 * c]);
+    split(__fmul2_rn(make_float2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), w0), &hi[2 * c + 1], &lo[2 * c + 1]);
+    w0 = w1;
+  }
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int x = 4 * y;
-      const float2 a = __fmul2_rn(make_float2(__uint_as_float(sc[x]), __uint_as_float(sc[x + 1])), w[y + 1]);
-      const float2 b = __fmul2_rn(make_float2(__uint_as_float(sc[x + 2]), __uint_as_float(sc[x + 3])), w[y]);
-      split(a, &m[2 * y], &l[2 * y]);
-      split(b, &m[2 * y + 1], &l[2 * y + 1]);
-    }
-    w0 = w2;
-    // matrices: (rows 0-7, block c), (rows 8-15, block c), (rows 0-7, block c + 1), (rows 8-15, block c + 1)
-    const uint32_t to = p_smem + row * 128 + (((c + (lane >> 4)) ^ (row & 7)) << 4);
-    ltc::stsm_x4(to, m[0], m[1], m[2], m[3]);
-    ltc::stsm_x4(to + C * 128, l[0], l[1], l[2], l[3]);
+  for (int y = 0; y < 16; ++y) {
+    x[y] = hi[y];
+    x[16 + y] = lo[y];
+    asm volatile("" : "+r"(x[y]), "+r"(x[16 + y]));      // made here, not behind the wait that follows
   }
 }
 
@@ -471,61 +501,57 @@ __device__ __forceinline__ void value_parts(uint32_t (&v)[PARTS][2][8], uint32_t
       for (int x = 0; x < 8; ++x) asm volatile("" : "+r"(v[part][h][x]));
 }
 
-// The output of a chunk, the 32 channels of this warp's lanes: OP + weight * OI, in 64 rows of 64 bytes of shared memory,
-// whose 16-byte pieces are exchanged as a 64-byte swizzled tensor store wants them.
-template <int D>
-__device__ __forceinline__ void write_out(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, const Item& it, int row, int r,
-                                          const float* wo, int k, int qd, int lane) {
-  tc::fence_after_sync();
-  if (32 * qd < D) {
-    const int q = lane & 3;
-    uint8_t* os = sm.o + qd * (C * 64);
-    if (lane == 0) tc::bulk_wait_read_all();     // the store of the last tile has left this buffer
-    __syncwarp();
+// The output of a chunk, the 32 channels of this warp's lanes: OP + weight * OI, in 64 rows of 64 bytes of shared memory
+// whose 16-byte pieces are exchanged as a 64-byte swizzled tensor store wants them.  Sixteen tokens at a time; `read` is called
+// when all accumulators have been read.
+template <class F>
+__device__ __forceinline__ void make_out(uint8_t* os, const float* wo, int qd, int lane, F read) {
+  const int q = lane & 3, tok = 8 * (lane >> 4) + (lane & 7);       // tok: the row whose address this lane gives
+  uint32_t oi[2][8], op[2][8];
+  auto load = [&](int grp) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {                                   // 16 channels: g and g + 8; two tokens each of two blocks
+      const uint32_t at = ((uint32_t)(32 * qd + 16 * h) << 16) + 16 * grp;
+      ltc::ld_16x256b_x2(at + T_OI, oi[h]);
+      ltc::ld_16x256b_x2(at + T_OP, op[h]);
+    }
+  };
 #pragma unroll 1
-    for (int x = 0; x < 4; ++x) {                // 16 channels, 32 tokens: two each of four blocks, channels g and g + 8
-      const int h = x & 1, tq = x >> 1;
-      const uint32_t at = ((uint32_t)(32 * qd + 16 * h) << 16) + 32 * tq;
-      uint32_t oi[16], op[16], m[8];
-      ltc::ld_16x256b_x4(at + T_OI, oi);
-      ltc::ld_16x256b_x4(at + T_OP, op);
-      tc::wait_ld();
+  for (int grp = 0; grp < 4; ++grp) {
+    load(grp);
+    const float2 w0 = *reinterpret_cast<const float2*>(&wo[16 * grp + 2 * q]);
+    const float2 w1 = *reinterpret_cast<const float2*>(&wo[16 * grp + 8 + 2 * q]);
+    tc::wait_ld();
+    if (grp == 3) read();
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float2 wt = *reinterpret_cast<const float2*>(&wo[32 * tq + 8 * b + 2 * q]);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t m[4];
 #pragma unroll
-        for (int y = 2 * b; y < 2 * b + 2; ++y) {
-          const float2 v = __ffma2_rn(make_float2(__uint_as_float(oi[2 * y]), __uint_as_float(oi[2 * y + 1])), wt,
-                                      make_float2(__uint_as_float(op[2 * y]), __uint_as_float(op[2 * y + 1])));
-          m[y] = ltc::pack_bf16(v.x, v.y);
-        }
+      for (int y = 0; y < 4; ++y) {
+        const float2 v = __ffma2_rn(make_float2(__uint_as_float(oi[h][2 * y]), __uint_as_float(oi[h][2 * y + 1])), y < 2 ? w0 : w1,
+                                    make_float2(__uint_as_float(op[h][2 * y]), __uint_as_float(op[h][2 * y + 1])));
+        m[y] = ltc::pack_bf16(v.x, v.y);
       }
-      // matrices: (channels + 0, block b), (+ 8, b), (+ 0, b + 1), (+ 8, b + 1); rows are tokens
-#pragma unroll
-      for (int b = 0; b < 4; b += 2) {
-        const int tok = 32 * tq + 8 * (b + (lane >> 4)) + (lane & 7), piece = 2 * h + ((lane >> 3) & 1);
-        ltc::stsm_x4_trans(smem_addr(os) + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4), m[2 * b], m[2 * b + 1], m[2 * b + 2],
-                           m[2 * b + 3]);
-      }
+      // matrices: (channels + 0, block 0), (+ 8, 0), (+ 0, 1), (+ 8, 1); rows are tokens
+      const int piece = 2 * h + ((lane >> 3) & 1);
+      ltc::stsm_x4_trans(smem_addr(os) + (16 * grp + tok) * 64 + ((piece ^ ((tok >> 1) & 3)) << 4), m[0], m[1], m[2], m[3]);
     }
-    tc::fence_before_sync();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&sm.o_empty);
-    if (r == C) {
-      if (lane == 0) ltc::tensor_store_2d(&maps.out[it.w], smem_addr(os), it.h * D + 32 * qd, row);
-    } else {
-      // the rows behind the end are not ours
-      const LinWalk& w = t.a.walk[it.w];
-      for (int y = lane; y < r * 4; y += 32) {
-        const int i = y >> 2, piece = y & 3;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(w.out) + (size_t)(row + i) * w.out_stride + it.h * D + 32 * qd + 8 * piece;
-        *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(os + i * 64 + ((piece ^ ((i >> 1) & 3)) << 4));
-      }
-    }
-    if (lane == 0) tc::bulk_commit_group();
-  } else if (lane == 0) {
-    tc::mbar_arrive(&sm.o_empty);
+  }
+}
+
+// What the state's part of token i's output is multiplied by: forwards A^(i + 1), backwards A^(rows - 1 - i); of a full
+// chunk, or (tail) of the sequence's last.
+__device__ __forceinline__ void out_weights(float* wo, int i, const LinTc& t, const Item& it, int tail) {
+  const int rows = tail ? it.rows(it.c1 - 1) : C;
+  wo[i] = decay_pow(clamp_log_decay(t.a.log_decay[it.h]), t.a.walk[it.w].back ? max(rows - 1 - i, 0) : i + 1);
+}
+
+// Rows r .. of a tile, by `threads` threads.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int r, int thread, int threads) {
+  for (int y = thread; y < (C - r) * (D / 8); y += threads) {
+    const int row = r + y / (D / 8), piece = y % (D / 8);
+    *reinterpret_cast<uint4*>(tile + (piece >> 3) * (C * 128) + row * 128 + (piece & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -556,29 +582,28 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       uint32_t v[PARTS][2][8];
       if (32 * qd < D) value_parts<PARTS>(v, smem_addr(sm.stage[s][2]), wv[r < C], r, th, qd, lane);
       if (r < C) {
-        // keys and values behind the sequence's end: zeros, for products of theirs with zeros must be zero
-        for (int y = tid; y < (C - r) * (D / 8); y += 128) {
-          const int row = r + y / (D / 8), piece = y % (D / 8);
-          *reinterpret_cast<uint4*>(sm.stage[s][1 + th] + (piece >> 3) * (C * 128) + row * 128 + (piece & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        }
+        // keys behind the sequence's end: zeros, for products of theirs with zeros must be zero
+        zero_rows<D>(sm.stage[s][1], r, tid + 128 * th, 256);
         fence_proxy_async_smem();
       }
-      if (k > 0 && !(ok = wait_all(&sm.u_full, (uint32_t)((k - 1) & 1)))) break;      // the last chunk's parts have been used
+      const int b = buffer_of<STATE_ONLY>(k);
+      // the parts that were there have been used
+      if (used_before<STATE_ONLY>(k) && !(ok = wait_all(&sm.u_full[b], phase_of<STATE_ONLY>(k) ^ 1u))) break;
       tc::fence_after_sync();
       if (32 * qd < D) {
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            ltc::st_16x128b_x4(((uint32_t)(32 * qd + 16 * h) << 16) + T_V + 32u * part + 16u * th, v[part][h]);
+            ltc::st_16x128b_x4(((uint32_t)(32 * qd + 16 * h) << 16) + t_v<STATE_ONLY>(k) + 32u * part + 16u * th,
+                               v[part][h]);
         }
         ltc::wait_st();
       }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(&sm.v_full);
+        tc::mbar_arrive(&sm.v_full[b]);
         tc::mbar_arrive(&sm.empty[s]);
       }
       if (++s == NST) {
@@ -607,9 +632,26 @@ __device__ void score_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     if (tc::named_sync_any(3, 128, !ok)) break;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       if (!(ok = wait_all(&sm.sc_full, (uint32_t)(k & 1)))) break;
+      tc::fence_after_sync();
+      uint32_t x[32];
+      tc::ld_16x256b_x8(((uint32_t)(32 * qd) << 16) + T_SC, x);
+      tc::wait_ld();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.sc_empty);
+      const int r = it.rows(chunk_at(it, back, c));
+      if (r < C) zero_rows<D>(sm.stage[k % NST][2], r, tid, 128);      // values behind the sequence's end, as the keys
+      make_p(x, pz + C, back ? -1 : 1, r, qd, lane);
       if (k > 0 && !(ok = wait_all(&sm.op_full, (uint32_t)((k - 1) & 1)))) break;     // the last P has been used
       tc::fence_after_sync();
-      make_p(smem_addr(sm.p), pz + C, back ? -1 : 1, it.rows(chunk_at(it, back, c)), qd, lane);
+      // matrices: (rows 0-7, block y), (rows 8-15, block y), (rows 0-7, block y + 1), (rows 8-15, block y + 1)
+      const uint32_t row = 16 * qd + (lane & 15), to = smem_addr(sm.p) + row * 128;
+#pragma unroll
+      for (int y = 0; y < 8; y += 2) {
+        const uint32_t piece = ((y + (lane >> 4)) ^ (row & 7)) << 4;
+        ltc::stsm_x4(to + piece, x[2 * y], x[2 * y + 1], x[2 * y + 2], x[2 * y + 3]);
+        ltc::stsm_x4(to + C * 128 + piece, x[16 + 2 * y], x[17 + 2 * y], x[18 + 2 * y], x[19 + 2 * y]);
+      }
       fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();
@@ -625,22 +667,46 @@ __device__ void out_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, in
   const int qd = warp & 3, tid = 32 * qd + lane;
   int k = 0, n_item = 0;
   bool ok = true;
+  uint8_t* os = sm.o[qd];
   for (int i = 0; i < item_rounds(t); ++i) {
     const Item it = item_of<false>(t, sm.order, i);
     if (it.chunks() == 0) continue;
-    const bool back = t.a.walk[it.w].back;
+    const LinWalk& w = t.a.walk[it.w];
     float(*wo)[C] = sm.wo[n_item & 1];
     ++n_item;
-    {
-      // forwards A^(i + 1), backwards A^(rows - 1 - i)
-      const int i = tid & (C - 1), rows = tid < C ? C : it.rows(it.c1 - 1);
-      wo[tid >> 6][i] = decay_pow(clamp_log_decay(t.a.log_decay[it.h]), back ? max(rows - 1 - i, 0) : i + 1);
-    }
+    out_weights(wo[tid >> 6], tid & 63, t, it, tid >> 6);
     if (tc::named_sync_any(4, 128, !ok)) break;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
-      const int ch = chunk_at(it, back, c), r = it.rows(ch);
+      const int ch = chunk_at(it, w.back, c), r = it.rows(ch), row = it.begin + ch * C;
+      if (lane == 0) tc::bulk_wait_read_all();     // the last tile's store has left the buffer
       if (!(ok = wait_all(&sm.op_full, (uint32_t)(k & 1)))) break;
-      write_out<D>(t, maps, sm, it, it.begin + ch * C, r, wo[r < C], k, qd, lane);
+      tc::fence_after_sync();
+      auto read = [&] {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.o_empty);
+      };
+      if (32 * qd >= D) {
+        read();
+        continue;
+      }
+      make_out(os, wo[r < C], qd, lane, read);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (r == C) {
+        if (lane == 0) {
+          ltc::tensor_store_2d(&maps.out[it.w], smem_addr(os), it.h * D + 32 * qd, row);
+          tc::bulk_commit_group();
+        }
+      } else {
+        // the rows behind the end are not ours
+        for (int y = lane; y < r * 4; y += 32) {
+          const int j = y >> 2, piece = y & 3;
+          uint16_t* dst = reinterpret_cast<uint16_t*>(w.out) + (size_t)(row + j) * w.out_stride + it.h * D + 32 * qd + 8 * piece;
+          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(os + j * 64 + ((piece ^ ((j >> 1) & 3)) << 4));
+        }
+        __syncwarp();
+      }
     }
   }
   if (lane == 0) tc::bulk_wait_all();
@@ -729,7 +795,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     const float g = clamp_log_decay(t.a.log_decay[it.h]);
     const float lost_full = expm1f(g * C), lost_tail = it.chunks() > 0 ? expm1f(g * (float)it.rows(it.c1 - 1)) : 0.f;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
-      const int r = it.rows(chunk_at(it, back, c));
+      const int ch = chunk_at(it, back, c), r = it.rows(ch);
       const uint32_t par = (uint32_t)(k & 1);
       if (c == 0 && !STATE_ONLY) {
         // the state before the first chunk; the last item's products have been waited for
@@ -750,19 +816,19 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
 #pragma unroll
         for (int j = 0; j < HC; ++j) asm volatile("" : "+f"(S[j]));
       }
-      if (!(ok = wait_all(&sm.u_full, par))) break;
+      if (!(ok = wait_all(&sm.u_full[buffer_of<STATE_ONLY>(k)], phase_of<STATE_ONLY>(k)))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int j0 = 0; j0 < HC; j0 += 16) {
         uint32_t u[16];
         if (mine) {
-          tc::ld_32x32b_x16(lane_addr + T_U + HC * half + j0, u);
+          tc::ld_32x32b_x16(lane_addr + t_u<STATE_ONLY>(k) + HC * half + j0, u);
           tc::wait_ld();
         }
         if (j0 + 16 == HC) {         // U may be written again
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.u_empty);
+          if (lane == 0) tc::mbar_arrive(&sm.u_empty[buffer_of<STATE_ONLY>(k)]);
         }
         if (mine) {
 #pragma unroll
@@ -776,8 +842,8 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       }
       if (STATE_ONLY) continue;
       if (!(ok = wait_all(&sm.op_full, par))) break;          // the last copy has been used
+      tc::fence_after_sync();
       if (c + 1 < it.chunks()) {
-        tc::fence_after_sync();
         if (mine) state_to_tmem<D>(S, lane_addr + T_S + (HC / 2) * half);
         tc::fence_before_sync();
         __syncwarp();
@@ -800,21 +866,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 9);              // the products, and the eight warps that read the values
+      mbar_init(&sm.empty[s], STATE_ONLY ? 9 : 10);     // the products' warps, and the eight that read the values
     }
     mbar_init(&sm.sc_full, 1);
     mbar_init(&sm.p_full, 4);
-    mbar_init(&sm.v_full, 8);
     mbar_init(&sm.s_full, 8);
-    mbar_init(&sm.u_full, 1);
-    mbar_init(&sm.u_empty, 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.v_full[b], 8);
+      mbar_init(&sm.u_full[b], 1);
+      mbar_init(&sm.u_empty[b], 8);
+    }
     mbar_init(&sm.op_full, 1);
     mbar_init(&sm.o_empty, 4);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sm.st_full[h], 1);
       mbar_init(&sm.st_done[h], 4);
     }
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
+    mbar_init(&sm.sc_empty, 4);
     fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(&sm.taddr, 512);
@@ -822,23 +892,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  // registers: 896 threads x 72 at launch hold 128 x (40 + 80 + 80 + 48 + 48 + 104 + 104)
+  // registers: 896 threads x 72 at launch hold 128 x (40 + 72 + 72 + 64 + 48 + 104 + 104)
   if (warp < 4) {
     ltc::regs_down<40>();
     if (warp == 0) {
       if (lane == 0) load_role<D, PARTS, STATE_ONLY>(t, maps, sm);
       __syncwarp();
     } else if (warp == 1) {
-      mma_role<D, PARTS, STATE_ONLY>(t, sm);
+      update_role<D, PARTS, STATE_ONLY>(t, sm, chunks_of_block<D, STATE_ONLY>(t, sm));
     } else if (warp == 2) {
       if (lane == 0) state_io_role<D, PARTS, STATE_ONLY>(t, maps, sm);
       __syncwarp();
+    } else if (!STATE_ONLY) {
+      output_mma_role<D>(t, sm, chunks_of_block<D, STATE_ONLY>(t, sm));
     }
   } else if (warp < 12) {
-    ltc::regs_up<80>();
     value_role<D, PARTS, STATE_ONLY>(t, sm, warp, lane);
   } else if (warp < 16) {
-    ltc::regs_down<48>();
+    ltc::regs_down<64>();
     if (!STATE_ONLY) score_role<D>(t, sm, warp, lane);
   } else if (warp < 20) {
     ltc::regs_down<48>();
@@ -856,8 +927,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // ---- chaining the stretches ----------------------------------------------------------
 // ws[s] (stretch s's own contribution) -> the state before stretch s, in the walk's order:
 //   run = S_in;  for s in order: (ws[s], run) = (run, A^tokens(s) run + ws[s]).
+// A thread chains four elements, the next stretches' loads in flight; with four times the elements and no loads ahead it
+// took 131 us where this takes about 10 (9 stretches of 32 heads, d = 128).
+constexpr int kChainAhead = 4;
 template <int D>
 __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constant__ LinTc t) {
+  __shared__ float decay[2];
   const int x = blockIdx.x;
   Item it;
   it.w = x % t.a.walks;
@@ -871,34 +946,39 @@ __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constan
   const int ns = min((nc + t.split.per - 1) / t.split.per, t.split.stretches);
   if (ns <= 1) return;
   const LinWalk& w = t.a.walk[it.w];
-  const double g = (double)clamp_log_decay(t.a.log_decay[it.h]);
-  float* ws = stretch_state(t, it);
+  if (threadIdx.x < 2) {
+    // every stretch but the sequence's last one is `per` chunks long
+    const double tokens = threadIdx.x ? it.len - (double)(ns - 1) * t.split.per * C : (double)t.split.per * C;
+    decay[threadIdx.x] = (float)exp((double)clamp_log_decay(t.a.log_decay[it.h]) * tokens);
+  }
+  __syncthreads();
+  const int y = (blockIdx.y * 256 + threadIdx.x) * 4;
+  float* ws = stretch_state(t, it) + y;
   const size_t st0 = ((size_t)it.n * t.a.H + it.h) * D * D;
-  // every stretch between the ends of a walk is `per` chunks long; the last one of the sequence may differ
-  const float a_full = (float)exp(g * (double)t.split.per * C);
-  const float a_last = (float)exp(g * (double)(it.len - (ns - 1) * t.split.per * C));
-  for (int y = (blockIdx.y * 256 + threadIdx.x) * 4; y < D * D; y += gridDim.y * 256 * 4) {
-    float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (w.S_in) {
-      if (w.swap) {
-        const int i = y / D, j = y % D;
-        run = make_float4(w.S_in[st0 + (size_t)j * D + i], w.S_in[st0 + (size_t)(j + 1) * D + i],
-                          w.S_in[st0 + (size_t)(j + 2) * D + i], w.S_in[st0 + (size_t)(j + 3) * D + i]);
-      } else {
-        run = *reinterpret_cast<const float4*>(w.S_in + st0 + y);
-      }
+  auto at = [&](int k) { return reinterpret_cast<float4*>(ws + (size_t)(w.back ? ns - 1 - k : k) * D * D); };
+  float4 run = make_float4(0.f, 0.f, 0.f, 0.f), own[kChainAhead];
+#pragma unroll
+  for (int k = 0; k < kChainAhead; ++k)
+    if (k + 1 < ns) own[k] = *at(k);
+  if (w.S_in) {
+    if (w.swap) {
+      const int i = y / D, j = y % D;
+      run = make_float4(w.S_in[st0 + (size_t)j * D + i], w.S_in[st0 + (size_t)(j + 1) * D + i],
+                        w.S_in[st0 + (size_t)(j + 2) * D + i], w.S_in[st0 + (size_t)(j + 3) * D + i]);
+    } else {
+      run = *reinterpret_cast<const float4*>(w.S_in + st0 + y);
     }
-    for (int k = 0; k < ns; ++k) {
-      const int s = w.back ? ns - 1 - k : k;
-      float4* at = reinterpret_cast<float4*>(ws + (size_t)s * D * D + y);
-      if (k + 1 < ns) {
-        const float4 own = *at;
-        *at = run;
-        const float a = s == ns - 1 ? a_last : a_full;
-        run = make_float4(fmaf(a, run.x, own.x), fmaf(a, run.y, own.y), fmaf(a, run.z, own.z), fmaf(a, run.w, own.w));
-      } else {
-        *at = run;
-      }
+  }
+  for (int k0 = 0; k0 < ns; k0 += kChainAhead) {
+#pragma unroll
+    for (int u = 0; u < kChainAhead; ++u) {
+      const int k = k0 + u;
+      if (k >= ns) break;
+      const float4 o = own[u];
+      if (k + kChainAhead + 1 < ns) own[u] = *at(k + kChainAhead);
+      *at(k) = run;
+      const float a = decay[(w.back ? ns - 1 - k : k) == ns - 1];
+      if (k + 1 < ns) run = make_float4(fmaf(a, run.x, o.x), fmaf(a, run.y, o.y), fmaf(a, run.z, o.z), fmaf(a, run.w, o.w));
     }
   }
 }
@@ -922,13 +1002,13 @@ EncodeFn encode_fn() {
   return encode;
 }
 
-// rows of `width` bf16, `stride` elements apart, in boxes of 64 rows of `inner` (64 or 32) elements
-bool make_map(CUtensorMap* m, const void* p, int64_t width, int64_t stride, int64_t rows, int inner) {
+// rows of `width` bf16, `stride` elements apart, in boxes of `high` rows of `inner` (64 or 32) elements
+bool make_map(CUtensorMap* m, const void* p, int64_t width, int64_t stride, int64_t rows, int inner, int high) {
   EncodeFn encode = encode_fn();
   if (!encode) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)inner, (cuuint32_t)C};
+  const cuuint32_t box[2] = {(cuuint32_t)inner, (cuuint32_t)high};
   const cuuint32_t estr[2] = {1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -953,17 +1033,16 @@ cudaError_t launch_tc(const LinTc& t0, const LinMaps& maps, cudaStream_t st) {
   LinTc t = t0;
   const size_t smem = sizeof(LinSmem<D>) + 1024;
   static_assert(sizeof(LinSmem<D>) + 1024 <= 232448, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(linattn_tc_kernel<D, PARTS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static bool allowed[2][64];
+  cudaError_t e = allow_shared(linattn_tc_kernel<D, PARTS, false>, (int)smem, allowed[0]);
   if (e != cudaSuccess) return e;
-  // as many blocks for each walk
-  const int64_t all = (int64_t)t.items * t.a.walks;
-  const unsigned blocks = (unsigned)(all < kSms ? all : kSms / t.a.walks * t.a.walks);
+  const unsigned blocks = (unsigned)(t.items < kSms ? t.items : kSms);
   if (t.split.stretches > 1) {
-    e = cudaFuncSetAttribute(linattn_tc_kernel<D, PARTS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_shared(linattn_tc_kernel<D, PARTS, true>, (int)smem, allowed[1]);
     if (e != cudaSuccess) return e;
     linattn_tc_kernel<D, PARTS, true><<<blocks, kTcThreads, smem, st>>>(t, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    linattn_chain_kernel<D><<<dim3((unsigned)(t.a.N * t.a.H * t.a.walks), D == 128 ? 4 : 1), 256, 0, st>>>(t);
+    linattn_chain_kernel<D><<<dim3((unsigned)(t.a.N * t.a.H * t.a.walks), D * D / 1024), 256, 0, st>>>(t);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   linattn_tc_kernel<D, PARTS, false><<<blocks, kTcThreads, smem, st>>>(t, maps);
@@ -1007,14 +1086,14 @@ cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, c
   t.ws = ws;
   const int64_t items = (int64_t)a.N * a.H * sp.stretches;
   if (items * a.walks > 0x7fff0000ll) return cudaErrorInvalidValue;
-  t.items = (int32_t)items;
+  t.items = (int32_t)(items * a.walks);
   // the tensors of all walks, each mapped once
   struct Seen { const void* p; int64_t stride; } seen[4];
   int n = 0;
   auto index = [&](const void* p, int64_t stride) {
     for (int i = 0; i < n; ++i)
       if (seen[i].p == p && seen[i].stride == stride) return i;
-    if (n == 4 || !make_map(&maps.in[n], p, (int64_t)a.H * a.D, stride, a.total, 64)) return -1;
+    if (n == 4 || !make_map(&maps.in[n], p, (int64_t)a.H * a.D, stride, a.total, 64, C)) return -1;
     seen[n] = Seen{p, stride};
     return n++;
   };
@@ -1023,7 +1102,7 @@ cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, c
     t.map_k[w] = index(a.walk[w].key, a.walk[w].key_stride);
     t.map_v[w] = index(a.walk[w].value, a.walk[w].value_stride);
     if (t.map_q[w] < 0 || t.map_k[w] < 0 || t.map_v[w] < 0) return cudaErrorInvalidValue;
-    if (!make_map(&maps.out[w], a.walk[w].out, (int64_t)a.H * a.D, a.walk[w].out_stride, a.total, 32)) return cudaErrorInvalidValue;
+    if (!make_map(&maps.out[w], a.walk[w].out, (int64_t)a.H * a.D, a.walk[w].out_stride, a.total, 32, C)) return cudaErrorInvalidValue;
   }
   for (int w = 0; w < a.walks; ++w) {
     if (a.walk[w].S_in && !make_state_map(&maps.s_in[w], a.walk[w].S_in, a.D, (int64_t)a.N * a.H, a.walk[w].swap)) return cudaErrorInvalidValue;

@@ -462,7 +462,8 @@ cudaError_t launch_l(const NormArgs& a, cudaStream_t st, int* blocks_out) {
   const int blocks = (int)(need < kBlocks ? need : kBlocks);
   if (blocks_out) *blocks_out = blocks;
   const int smem = kStages * (BACK ? 2 : 1) * U * (BF16 ? 1 : 2) * kThreads * 16;
-  const cudaError_t e = cudaFuncSetAttribute(qk_norm_kernel<BF16, VEC, LL, U, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static bool allowed[64];
+  const cudaError_t e = allow_shared(qk_norm_kernel<BF16, VEC, LL, U, BACK>, smem, allowed);
   if (e != cudaSuccess) return e;
   qk_norm_kernel<BF16, VEC, LL, U, BACK><<<blocks, kThreads, smem, st>>>(a, n);
   return cudaGetLastError();
