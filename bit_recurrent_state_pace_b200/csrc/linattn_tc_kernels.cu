@@ -84,8 +84,9 @@ struct alignas(1024) LinSmem {
   uint8_t st[STATE];                                     // states on their way in and out: rows of 128 bytes, swizzled
   uint8_t o[4][C * 64];                                  // outputs on their way: 64 rows of 32 channels for each lane quadrant
   // tables of the decay, of two items in turn, each group of warps its own:
-  float wv[2][2][2][C];                                  // warps 4-7, 8-11: decay of a token's value in the state behind a
-                                                         // full chunk, and behind the sequence's last one (zeros beyond it)
+  uint2 wv[2][2][2][C / 4];                              // warps 4-7, 8-11: decay of their tokens' values in the state behind
+                                                         // a full chunk, and behind the sequence's last one (zeros beyond
+                                                         // it): two tokens an entry, as value_parts wants them
   float pz[2][2 * C + 8];                                // warps 12-15: A^n at [C + n], zeros below
   float wo[2][2][C];                                     // warps 16-19: of the state in a token's output, as wv
   uint64_t full[NST], empty[NST];
@@ -452,10 +453,17 @@ __device__ __forceinline__ void make_p(uint32_t (&x)[32], const float* pz, int s
 }
 
 // Tokens 32 th .. + 31 of the value tile, times their decay, transposed for TMEM lanes 32 qd .. + 31 (channels), two
-// tokens a word, in three bf16 parts.  The parts are cut off, not rounded: 8 bits each of the product's 24, so that
-// their sum is the product.  v[part][16 channels of h][..]: words of token groups 0..3, channels g and g + 8.
+// tokens a word, in PARTS bf16 parts.  v[part][16 channels of h][..]: words of token groups 0..3, channels g and g + 8.
+//
+// Three parts: the product in fp32 (wv: the two tokens' decays), cut off, not rounded: 8 bits each of its 24, so that
+// their sum is the product.
+//
+// Two parts, all in packed bf16 (wv: both decays' first 8 bits w1, the next w2): x w1 = hi + r exactly (the rest of a
+// rounded product fits bf16 and a fused multiply-add gives it), and mid = x w2 + r holds the product to 2^-17.  That is
+// a third of the instructions; for three parts it would be as many as in fp32, with more registers (all spilled: 64
+// ragged prompts 228 -> 276 us).
 template <int PARTS>
-__device__ __forceinline__ void value_parts(uint32_t (&v)[PARTS][2][8], uint32_t tile, const float* wv, int r, int th, int qd,
+__device__ __forceinline__ void value_parts(uint32_t (&v)[PARTS][2][8], uint32_t tile, const uint2* wv, int r, int th, int qd,
                                             int lane) {
   const int q = lane & 3;
   // lane's row address of an ldmatrix: matrix lane / 8 = (channels + 8 (m & 1), tokens + 8 (m >> 1)), row lane % 8
@@ -476,29 +484,33 @@ __device__ __forceinline__ void value_parts(uint32_t (&v)[PARTS][2][8], uint32_t
         v[0][h][x] = i >= r ? 0u : (i + 1 >= r ? v[0][h][x] & 0xffffu : v[0][h][x]);
       }
   }
+  using B2 = __nv_bfloat162;
+  auto b2 = [](uint32_t u) { return *reinterpret_cast<const B2*>(&u); };
+  auto u32 = [](B2 b) { return *reinterpret_cast<const uint32_t*>(&b); };
   const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    const float2 w = *reinterpret_cast<const float2*>(wv + 32 * th + 8 * (x >> 1) + 2 * q);
+  for (int x = 0; x < 8; ++x) {                // tokens 8 (x >> 1) + 2 q, + 1
+    const uint2 w = wv[4 * (x >> 1) + q];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float2 p = __fmul2_rn(make_float2(ltc::bf16_lo(v[0][h][x]), ltc::bf16_hi(v[0][h][x])), w);
+      const uint32_t e = v[0][h][x];
+      if (PARTS == 2) {
+        const B2 hi = __hmul2_rn(b2(e), b2(w.x));
+        v[0][h][x] = u32(hi);
+        v[1][h][x] = u32(__hfma2(b2(e), b2(w.y), __hfma2(b2(e), b2(w.x), __hneg2(hi))));
+      } else {
+        float2 p = __fmul2_rn(make_float2(ltc::bf16_lo(e), ltc::bf16_hi(e)),
+                              make_float2(__uint_as_float(w.x), __uint_as_float(w.y)));
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part) {
-        const uint32_t a0 = __float_as_uint(p.x), a1 = __float_as_uint(p.y);
-        v[part][h][x] = ltc::upper_halves(a0, a1);
-        if (part + 1 < PARTS)
-          p = __ffma2_rn(make_float2(__uint_as_float(a0 & 0xffff0000u), __uint_as_float(a1 & 0xffff0000u)), minus, p);
+        for (int part = 0; part < PARTS; ++part) {
+          const uint32_t a0 = __float_as_uint(p.x), a1 = __float_as_uint(p.y);
+          v[part][h][x] = ltc::upper_halves(a0, a1);
+          if (part + 1 < PARTS)
+            p = __ffma2_rn(make_float2(__uint_as_float(a0 & 0xffff0000u), __uint_as_float(a1 & 0xffff0000u)), minus, p);
+        }
       }
     }
   }
-  // made here, not behind the wait that follows
-#pragma unroll
-  for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int x = 0; x < 8; ++x) asm volatile("" : "+r"(v[part][h][x]));
 }
 
 // The output of a chunk, the 32 channels of this warp's lanes: OP + weight * OI, in 64 rows of 64 bytes of shared memory
@@ -567,13 +579,24 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     const Item it = item_of<STATE_ONLY>(t, sm.order, i);
     if (it.chunks() == 0) continue;
     const bool back = t.a.walk[it.w].back;
-    float(*wv)[C] = sm.wv[n_item & 1][th];
+    uint2(*wv)[C / 4] = sm.wv[n_item & 1][th];
     ++n_item;
-    {
+    if (tid < C / 2) {
       // forwards A^(rows - 1 - i), backwards A^(i + 1)
       const float g = clamp_log_decay(t.a.log_decay[it.h]);
-      const int i = tid & (C - 1), tail = tid >> 6, rows = tail ? it.rows(it.c1 - 1) : C;
-      wv[tail][i] = i < rows ? decay_pow(g, back ? i + 1 : rows - 1 - i) : 0.f;
+      const int tail = tid >> 4, rows = tail ? it.rows(it.c1 - 1) : C;
+      float w[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = 32 * th + 2 * (tid & 15) + y;
+        w[y] = i < rows ? decay_pow(g, back ? i + 1 : rows - 1 - i) : 0.f;
+      }
+      uint2 e = make_uint2(__float_as_uint(w[0]), __float_as_uint(w[1]));
+      if (PARTS == 2) {
+        e.x = ltc::pack_bf16(w[0], w[1]);
+        e.y = ltc::pack_bf16(w[0] - ltc::bf16_lo(e.x), w[1] - ltc::bf16_hi(e.x));
+      }
+      wv[tail][tid & 15] = e;
     }
     if (tc::named_sync_any(1 + th, 128, !ok)) break;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
