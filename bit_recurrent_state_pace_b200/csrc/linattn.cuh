@@ -37,6 +37,39 @@ struct LinArgs {
   LinWalk walk[kLinMaxWalks];
 };
 
+// How every sequence is cut into stretches that run side by side where sequences and heads alone would leave SMs idle:
+// stretch s is its chunks (of kLinChunk tokens) [s per, (s + 1) per), the last one what is left.  A first pass over all
+// but the last gives each one's own contribution to the state, the chain kernel turns those into the states before each
+// stretch, and the stretches then run from these.
+constexpr int kLinChunk = 64;
+struct LinSplit {
+  int32_t stretches;        // at most, for one sequence
+  int32_t per;              // chunks a stretch
+};
+// Stretches of a sequence of `len` tokens (one for an empty one).
+__device__ __forceinline__ int stretches_of(const LinSplit& sp, int len) {
+  const int nc = (int)(((int64_t)len + kLinChunk - 1) / kLinChunk), ns = (nc + sp.per - 1) / sp.per;
+  return ns < 1 ? 1 : (ns > sp.stretches ? sp.stretches : ns);
+}
+// The stretches' states: ws[walk][n][h][stretch][D][D], fp32, in the walk's own order of rows.
+__device__ __forceinline__ int64_t stretch_index(const LinArgs& a, const LinSplit& sp, int w, int n, int h, int seg) {
+  return (((int64_t)w * a.N + n) * a.H + h) * sp.stretches + seg;
+}
+// `items` run side by side uncut and `fill` of them fill the SMs.  Stretches of `least` chunks at least; fewer than `few`
+// of them are not worth the first pass.
+inline LinSplit lin_split(int64_t items, int64_t max_len, int64_t fill, int least, int few) {
+  const int64_t chunks = (max_len + kLinChunk - 1) / kLinChunk;
+  LinSplit sp;
+  sp.stretches = 1;
+  sp.per = (int32_t)(chunks < 1 ? 1 : chunks);
+  int64_t n = fill / items;
+  if (n > chunks / least) n = chunks / least;
+  if (n < few) return sp;
+  sp.per = (int32_t)((chunks + n - 1) / n);
+  sp.stretches = (int32_t)((chunks + sp.per - 1) / sp.per);
+  return sp;
+}
+
 // Rows [begin, end) of sequence n, inside [0, total] whatever cu holds.
 __device__ __forceinline__ void seq_rows(const LinArgs& a, int n, int* begin, int* end) {
   if (a.cu) {
@@ -68,7 +101,10 @@ inline cudaError_t allow_shared(K kernel, int bytes, bool (&done)[64]) {
   return e;
 }
 
-cudaError_t launch_linattn_stream(const LinArgs& a, cudaStream_t st);
+// The walk token by token; ws: of sp.stretches > 1.
+LinSplit linattn_stream_split(int64_t heads, int64_t max_len, int walks, int D);
+cudaError_t launch_linattn_stream(const LinArgs& a, const LinSplit& sp, float* ws, cudaStream_t st);
+cudaError_t launch_linattn_chain(const LinArgs& a, const LinSplit& sp, float* ws, cudaStream_t st);
 cudaError_t launch_linattn_step(float* S, const void* q, const void* k, const void* v, const float* log_decay, void* o,
                                 int64_t qs, int64_t ks, int64_t vs, int64_t os, int N, int H, int D, int io,
                                 cudaStream_t st);

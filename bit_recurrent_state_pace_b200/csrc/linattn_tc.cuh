@@ -143,14 +143,6 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 
 }  // namespace ltc
 
-// How the chunks of every sequence are cut into stretches that run side by
-// side: stretch s of a sequence is its chunks [s per, (s + 1) per), the last
-// one taking what is left.
-struct LinSplit {
-  int32_t stretches;        // at most, for one sequence
-  int32_t per;              // chunks a stretch
-};
-
 LinSplit linattn_tc_split(int64_t heads, int64_t max_len, int walks);
 bool linattn_tc_takes(const LinArgs& a);
 cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, cudaStream_t st);

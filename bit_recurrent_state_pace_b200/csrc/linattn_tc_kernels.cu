@@ -131,8 +131,7 @@ __device__ __forceinline__ Item item_of(const LinTc& t, const uint16_t* order, i
   seq_rows(t.a, it.n, &it.begin, &end);
   it.len = end - it.begin;
   const int nc = (it.len + C - 1) / C;
-  int ns = (nc + t.split.per - 1) / t.split.per;
-  it.nseg = ns < 1 ? 1 : (ns > t.split.stretches ? t.split.stretches : ns);
+  it.nseg = stretches_of(t.split, it.len);
   it.on = there && it.seg < it.nseg;
   // the stretch that a walk ends with hands its state to no other
   if (STATE_ONLY) it.on = it.on && it.seg != (t.a.walk[it.w].back ? 0 : it.nseg - 1);
@@ -140,13 +139,6 @@ __device__ __forceinline__ Item item_of(const LinTc& t, const uint16_t* order, i
   it.c1 = it.seg == it.nseg - 1 ? nc : it.c0 + t.split.per;
   if (!it.on) it.c0 = it.c1 = 0;
   return it;
-}
-// index of a stretch's state in ws, in states
-__device__ __forceinline__ int stretch_index(const LinTc& t, const Item& it) {
-  return ((it.w * t.a.N + it.n) * t.a.H + it.h) * t.split.stretches + it.seg;
-}
-__device__ __forceinline__ float* stretch_state(const LinTc& t, const Item& it) {
-  return t.ws + (size_t)stretch_index(t, it) * t.a.D * t.a.D;
 }
 // What an item begins from and leaves: a state of ws, of the walk's tensors (transposed or not), or none.
 struct StateIo {
@@ -244,7 +236,7 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
       return;
     }
     const CUtensorMap* m = it.nseg > 1 ? &maps.ws : &maps.s_in[it.w];
-    const int row = (it.nseg > 1 ? stretch_index(t, it) : it.n * t.a.H + it.h) * D;
+    const int row = (it.nseg > 1 ? (int)stretch_index(t.a, t.split, it.w, it.n, it.h, it.seg) : it.n * t.a.H + it.h) * D;
     mbar_arrive_expect_tx(&sm.st_full[half], LinSmem<D>::STATE);
     const int boxes = swap ? D / 32 : D / 64, bytes = swap ? D * 64 : D * 128;
     for (int b = 0; b < boxes; ++b)
@@ -255,7 +247,7 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
     if (!ltc::wait_tries(&sm.st_done[half], round[half]++ & 1u)) return false;
     if (out) {
       const CUtensorMap* m = STATE_ONLY ? &maps.ws : &maps.s_out[it.w];
-      const int row = (STATE_ONLY ? stretch_index(t, it) : it.n * t.a.H + it.h) * D;
+      const int row = (STATE_ONLY ? (int)stretch_index(t.a, t.split, it.w, it.n, it.h, it.seg) : it.n * t.a.H + it.h) * D;
       const int boxes = swap ? D / 32 : D / 64, bytes = swap ? D * 64 : D * 128;
       for (int b = 0; b < boxes; ++b)
         ltc::tensor_store_2d(m, smem_addr(sm.st) + b * bytes, 32 * b + (swap ? 0 : D / 2 * half), row + (swap ? D / 2 * half : 0));
@@ -947,65 +939,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 1) tc::tmem_free(sm.taddr, 512);
 }
 
-// ---- chaining the stretches ----------------------------------------------------------
-// ws[s] (stretch s's own contribution) -> the state before stretch s, in the walk's order:
-//   run = S_in;  for s in order: (ws[s], run) = (run, A^tokens(s) run + ws[s]).
-// A thread chains four elements, the next stretches' loads in flight; with four times the elements and no loads ahead it
-// took 131 us where this takes about 10 (9 stretches of 32 heads, d = 128).
-constexpr int kChainAhead = 4;
-template <int D>
-__global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constant__ LinTc t) {
-  __shared__ float decay[2];
-  const int x = blockIdx.x;
-  Item it;
-  it.w = x % t.a.walks;
-  it.h = (x / t.a.walks) % t.a.H;
-  it.n = x / t.a.walks / t.a.H;
-  it.seg = 0;
-  int end;
-  seq_rows(t.a, it.n, &it.begin, &end);
-  it.len = end - it.begin;
-  const int nc = (it.len + C - 1) / C;
-  const int ns = min((nc + t.split.per - 1) / t.split.per, t.split.stretches);
-  if (ns <= 1) return;
-  const LinWalk& w = t.a.walk[it.w];
-  if (threadIdx.x < 2) {
-    // every stretch but the sequence's last one is `per` chunks long
-    const double tokens = threadIdx.x ? it.len - (double)(ns - 1) * t.split.per * C : (double)t.split.per * C;
-    decay[threadIdx.x] = (float)exp((double)clamp_log_decay(t.a.log_decay[it.h]) * tokens);
-  }
-  __syncthreads();
-  const int y = (blockIdx.y * 256 + threadIdx.x) * 4;
-  float* ws = stretch_state(t, it) + y;
-  const size_t st0 = ((size_t)it.n * t.a.H + it.h) * D * D;
-  auto at = [&](int k) { return reinterpret_cast<float4*>(ws + (size_t)(w.back ? ns - 1 - k : k) * D * D); };
-  float4 run = make_float4(0.f, 0.f, 0.f, 0.f), own[kChainAhead];
-#pragma unroll
-  for (int k = 0; k < kChainAhead; ++k)
-    if (k + 1 < ns) own[k] = *at(k);
-  if (w.S_in) {
-    if (w.swap) {
-      const int i = y / D, j = y % D;
-      run = make_float4(w.S_in[st0 + (size_t)j * D + i], w.S_in[st0 + (size_t)(j + 1) * D + i],
-                        w.S_in[st0 + (size_t)(j + 2) * D + i], w.S_in[st0 + (size_t)(j + 3) * D + i]);
-    } else {
-      run = *reinterpret_cast<const float4*>(w.S_in + st0 + y);
-    }
-  }
-  for (int k0 = 0; k0 < ns; k0 += kChainAhead) {
-#pragma unroll
-    for (int u = 0; u < kChainAhead; ++u) {
-      const int k = k0 + u;
-      if (k >= ns) break;
-      const float4 o = own[u];
-      if (k + kChainAhead + 1 < ns) own[u] = *at(k + kChainAhead);
-      *at(k) = run;
-      const float a = decay[(w.back ? ns - 1 - k : k) == ns - 1];
-      if (k + 1 < ns) run = make_float4(fmaf(a, run.x, o.x), fmaf(a, run.y, o.y), fmaf(a, run.z, o.z), fmaf(a, run.w, o.w));
-    }
-  }
-}
-
+// ---- launch ----------------------------------------------------------------------------
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1065,8 +999,7 @@ cudaError_t launch_tc(const LinTc& t0, const LinMaps& maps, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     linattn_tc_kernel<D, PARTS, true><<<blocks, kTcThreads, smem, st>>>(t, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    linattn_chain_kernel<D><<<dim3((unsigned)(t.a.N * t.a.H * t.a.walks), D * D / 1024), 256, 0, st>>>(t);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_linattn_chain(t.a, t.split, t.ws, st)) != cudaSuccess) return e;
   }
   linattn_tc_kernel<D, PARTS, false><<<blocks, kTcThreads, smem, st>>>(t, maps);
   return cudaGetLastError();
@@ -1075,18 +1008,9 @@ cudaError_t launch_tc(const LinTc& t0, const LinMaps& maps, cudaStream_t st) {
 }  // namespace
 
 LinSplit linattn_tc_split(int64_t heads, int64_t max_len, int walks) {
-  LinSplit sp;
-  sp.stretches = 1;
-  const int64_t chunks = (max_len + C - 1) / C, items = heads * walks;
-  sp.per = (int32_t)(chunks < 1 ? 1 : chunks);
-  if (items >= kSms || chunks < 16) return sp;
+  const int64_t items = heads * walks;
   // stretches of 8 chunks at least, two rounds of the SMs at most
-  int64_t n = 2 * kSms / items;
-  if (n > chunks / 8) n = chunks / 8;
-  if (n < 2) return sp;
-  sp.per = (int32_t)((chunks + n - 1) / n);
-  sp.stretches = (int32_t)((chunks + sp.per - 1) / sp.per);
-  return sp;
+  return lin_split(items, max_len, items >= kSms ? 0 : 2 * kSms, 8, 2);
 }
 
 bool linattn_tc_takes(const LinArgs& a) {

@@ -66,9 +66,13 @@ pace::LinArgs lin_args(const pace_linattn_desc* d, const float* log_decay, const
   return a;
 }
 
-// Walks over all sequences, on the tensor cores where their shapes allow.
+// Walks over all sequences, on the tensor cores where their shapes allow.  The workspace depends on the desc alone: where
+// alignment keeps a shape that the tensor cores would take off them, the sequences are not cut.
+inline bool tc_shape(const pace_linattn_desc* d) { return d->io_dtype == PACE_IO_BF16 && d->d_k >= 64; }
 inline pace::LinSplit split_of(const pace_linattn_desc* d, int walks) {
-  return pace::linattn_tc_split((int64_t)d->num_seqs * d->num_heads, d->max_len, walks);
+  const int64_t heads = (int64_t)d->num_seqs * d->num_heads;
+  return tc_shape(d) ? pace::linattn_tc_split(heads, d->max_len, walks)
+                     : pace::linattn_stream_split(heads, d->max_len, walks, d->d_k);
 }
 inline size_t stretch_bytes(const pace_linattn_desc* d, int walks) {
   const pace::LinSplit sp = split_of(d, walks);
@@ -76,10 +80,16 @@ inline size_t stretch_bytes(const pace_linattn_desc* d, int walks) {
   return (size_t)walks * d->num_seqs * d->num_heads * sp.stretches * d->d_k * d->d_k * sizeof(float);
 }
 pace_status run_walks(const pace_linattn_desc* d, const pace::LinArgs& a, void* ws, cudaStream_t st) {
-  if (!pace::linattn_tc_takes(a)) return from_cuda(pace::launch_linattn_stream(a, st));
   const pace::LinSplit sp = split_of(d, a.walks);
+  float* states = reinterpret_cast<float*>(ws);
+  const bool tc = pace::linattn_tc_takes(a);
+  if (tc_shape(d) && !tc) {
+    pace::LinSplit whole = sp;
+    whole.stretches = 1;
+    return from_cuda(pace::launch_linattn_stream(a, whole, nullptr, st));
+  }
   if (sp.stretches > 1 && !ws) return PACE_ERR_INVALID_ARG;
-  return from_cuda(pace::launch_linattn_tc(a, sp, reinterpret_cast<float*>(ws), st));
+  return from_cuda(tc ? pace::launch_linattn_tc(a, sp, states, st) : pace::launch_linattn_stream(a, sp, states, st));
 }
 
 struct NormShape { int64_t qs, ks, qo, ko; size_t esz; };
@@ -135,8 +145,7 @@ pace_status pace_linattn_workspace_bytes(const pace_linattn_desc* desc, int32_t 
   if (!bytes || (backward != 0 && backward != 1)) return PACE_ERR_INVALID_ARG;
   const pace_status st = check_lin(desc, &s, true);
   if (st != PACE_OK) return st;
-  *bytes = 0;
-  if (desc->io_dtype == PACE_IO_BF16 && desc->d_k >= 64) *bytes = stretch_bytes(desc, backward ? 3 : 1);
+  *bytes = stretch_bytes(desc, backward ? 3 : 1);
   return PACE_OK;
 }
 

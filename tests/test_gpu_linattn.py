@@ -47,10 +47,16 @@ def state_tol(bound, longest, d):
     return ref.roundings32(longest, d) * ref.U32 * bound
 
 
+# The tolerances count relative half steps, which subnormal numbers do not keep to: there a rounding is off by half a
+# step of 2^-149 (fp32) or 2^-133 (a bf16 part), whatever the number.  At most roundings32(5000, 128) < 2^15 of them, each
+# times a further factor below 2^3 (inputs of these tests), add up to less than 2^(15 - 134 + 3).
+TINY = 2.0 ** -116
+
+
 def close(got, want, tol):
     got = f64(got)
     assert np.isfinite(got).all()
-    over = np.abs(got - want) - tol
+    over = np.abs(got - want) - tol - TINY
     assert over.max(initial=-1.0) <= 0, (float(over.max()), np.unravel_index(over.argmax(), over.shape))
 
 
@@ -371,3 +377,108 @@ def test_flags_stay_clear_and_bad_tensors_are_refused():
                  lambda: pace.pace_linattn_step(S0, q, k, v, g)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_stretches_of_ragged_sequences(d, dt):
+    """Few heads and one long sequence beside short and empty ones: some are cut into stretches, their ends inside, at and
+    one behind a chunk; ST over S0."""
+    dt, H, lens = DT[dt], 2, [1100, 0, 1, 64, 513, 640, 65]
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    q, k, v, do, S0, dST = make(int(cu[-1]), H, d, dt, len(lens), seed=7)
+    g, dev_cu = torch.tensor([-0.05, -0.0007], device="cuda"), torch.from_numpy(cu.astype(np.int32)).cuda()
+    assert pace.pace_linattn_workspace_bytes(len(lens), H, d, pace.PACE_IO_F32 if dt == torch.float32 else pace.PACE_IO_BF16,
+                                             int(cu[-1]), 1100, False) > 0
+    ST = S0.clone()
+    o, _ = pace.pace_linattn_forward(q, k, v, g, cu_seqlens=dev_cu, max_len=1100, S0=ST, ST=ST)
+    check_forward(q, k, v, g, S0, cu, o, ST, dt)
+    grads = pace.pace_linattn_backward(q, k, v, g, do, cu_seqlens=dev_cu, max_len=1100, S0=S0, dST=dST)
+    check_backward(q, k, v, g, S0, do, dST, cu, grads, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [512, 513, 700])
+def test_many_sequences(n, dt):
+    """More short sequences than blocks, around the number up to which they are sorted, with states in and out."""
+    dt, H, d = DT[dt], 2, 64
+    lens = np.random.default_rng(n).integers(0, 100, n)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    q, k, v, do, S0, dST = make(int(cu[-1]), H, d, dt, n, seed=n)
+    g, dev_cu = torch.tensor([-0.2, -0.01], device="cuda"), torch.from_numpy(cu.astype(np.int32)).cuda()
+    o, ST = pace.pace_linattn_forward(q, k, v, g, cu_seqlens=dev_cu, max_len=100, S0=S0)
+    check_forward(q, k, v, g, S0, cu, o, ST, dt)
+    grads = pace.pace_linattn_backward(q, k, v, g, do, cu_seqlens=dev_cu, max_len=100, S0=S0, dST=dST)
+    check_backward(q, k, v, g, S0, do, dST, cu, grads, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_decays_of_every_size(d, dt):
+    """Decays whose powers leave the range of fp32 within a chunk, within a few tokens, and ones that round to 1."""
+    dt, T = DT[dt], 210
+    g = torch.tensor([-1.3, -2.999, -3.001, -45.0, -88.0, -104.0, -1e30, -1e-8], device="cuda")
+    H, cu = g.numel(), np.array([0, 150, T])
+    q, k, v, do, S0, dST = make(T, H, d, dt, 2, seed=4)
+    dev_cu = torch.from_numpy(cu.astype(np.int32)).cuda()
+    o, ST = pace.pace_linattn_forward(q, k, v, g, cu_seqlens=dev_cu, max_len=150, S0=S0)
+    check_forward(q, k, v, g, S0, cu, o, ST, dt)
+    for s, t in ((S0, dST), (None, None)):
+        grads = pace.pace_linattn_backward(q, k, v, g, do, cu_seqlens=dev_cu, max_len=150, S0=s, dST=t)
+        check_backward(q, k, v, g, s, do, t, cu, grads, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_two_graphs_and_an_eager_call(dt):
+    """Two captured graphs, replayed in turn with eager calls between them, keep to their own workspaces."""
+    dt, T, H, d = DT[dt], 2000, 1, 64
+    g = decays(H)
+    sets = [make(T, H, d, dt, 1, seed=s) for s in (1, 2, 3)]
+
+    def all_of(q, k, v, do, S0, dST):
+        return (pace.pace_linattn_forward(q, k, v, g, S0=S0) + pace.pace_linattn_backward(q, k, v, g, do, S0=S0, dST=dST))
+
+    want = [all_of(*x) for x in sets]
+    graphs, held = [], []
+    for x in sets[:2]:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(all_of(*x))
+    for _ in range(2):
+        graphs[0].replay()
+        eager = all_of(*sets[2])
+        graphs[1].replay()
+        graphs[0].replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, held + [eager]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_a_layer_under_autograd():
+    """Both directions as one autograd function, with shared key/value heads: the gradient of the shared heads is the
+    sum over the query heads that read them."""
+    n, T, H, d, dt = 2, 70, 4, 64, torch.float32
+
+    class Retain(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, g):
+            ctx.save_for_backward(q, k, v, g)
+            return pace.pace_linattn_forward(q, k, v, g, num_seqs=n)[0]
+
+        @staticmethod
+        def backward(ctx, do):
+            q, k, v, g = ctx.saved_tensors
+            return (*pace.pace_linattn_backward(q, k, v, g, do.contiguous(), num_seqs=n)[:3], None)
+
+    q, _, v, do, _, _ = make(n * T, H, d, dt, n, seed=6, states=False)
+    k = make(n * T, 2, d, dt, n, seed=8, states=False)[1]
+    g, cu = decays(H), np.arange(n + 1) * T
+    for x in (q, k, v):
+        x.requires_grad_()
+    shared = k.repeat_interleave(2, 1)
+    Retain.apply(q, shared, v, g).backward(do)
+    (wq, bq), (wk, bk), (wv, bv), _ = ref.backward(f64(q), f64(shared), f64(v), f64(g), zeros(n, H, d), f64(do), zeros(n, H, d), cu)
+    close(q.grad, wq, io_tol(bq, wq, dt, T, d))
+    close(v.grad, wv, io_tol(bv, wv, dt, T, d))
+    pair = lambda x: x.reshape(n * T, 2, 2, d).sum(2)  # noqa: E731
+    close(k.grad, pair(wk), io_tol(pair(bk), pair(wk), dt, T, d) + ref.U32 * pair(bk))
