@@ -12,6 +12,7 @@ Importing this package loads ``libpace.so`` from this directory and raises
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -448,8 +449,23 @@ def _run(name: str, fn, index: int, stream, *args) -> None:
 _plans: dict = {}
 
 
+def _whole(name: str, x) -> Optional[int]:
+    """An optional integer as one: nothing else (a tensor, say) becomes part of a plan's key."""
+    if x is None or type(x) is int:
+        return x
+    try:
+        return operator.index(x)
+    except TypeError:
+        raise ValueError(f"{name}: an integer, not {type(x).__name__}") from None
+
+
 def _form(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+    if t is None:
+        return None
+    try:
+        return t.shape, t.stride(), t.dtype, t.get_device()
+    except AttributeError:
+        return type(t)                           # no tensor: the checks of a first call refuse it
 
 
 def _plan(key, build):
@@ -543,6 +559,7 @@ def pace_linattn_forward(q, k, v, log_decay, o=None, ST=None, num_seqs=None, max
     cu_seqlens: int32 [N + 1], or None for prompts of one length; S0, ST: fp32 [N, H, d, d].  Rows of no sequence
     are left as they are (unset in an o made here).
     """
+    num_seqs, max_len = _whole("num_seqs", num_seqs), _whole("max_len", max_len)
 
     def build():
         _tensors(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("o", o), ("ST", ST), ("cu_seqlens", cu_seqlens),
@@ -576,6 +593,7 @@ def pace_linattn_backward(q, k, v, log_decay, d_o, dq=None, dk=None, dv=None, dS
 
     dq, dk, dv have the row strides of q, k, v; those not given are made so (rows of no sequence are left unset).
     """
+    num_seqs, max_len = _whole("num_seqs", num_seqs), _whole("max_len", max_len)
 
     def build():
         _tensors(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("d_o", d_o), ("dq", dq), ("dk", dk), ("dv", dv),
@@ -681,6 +699,7 @@ def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_
 
     q: [tokens, Hq, d], k: [tokens, Hk, d] (either may be None); q_out may be q, k_out may be k.
     """
+    rotary_dim, interleaved, eps, q_scale = _whole("rotary_dim", rotary_dim) or 0, bool(interleaved), float(eps), float(q_scale)
 
     def build():
         _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),
@@ -722,6 +741,7 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
                                  q_scale=1.0, workspace=None, stream=None):
     """Gradients of pace_qk_norm_rotate: returns (dq, dk, dq_weight, dk_weight); a weight's gradient is made where the
     weight is given (or a tensor for it)."""
+    rotary_dim, interleaved, eps, q_scale = _whole("rotary_dim", rotary_dim) or 0, bool(interleaved), float(eps), float(q_scale)
 
     def build():
         _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),

@@ -130,7 +130,7 @@ struct NormArgs {
   float* partial;           // [blocks][2][D], backward with weight gradients
 };
 
-size_t qk_norm_partial_bytes(int64_t tokens, int D);
+size_t qk_norm_partial_bytes(int D);
 cudaError_t launch_qk_norm(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_qk_norm_backward(const NormArgs& a, cudaStream_t st);
 

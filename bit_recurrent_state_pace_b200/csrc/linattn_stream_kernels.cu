@@ -372,10 +372,10 @@ cudaError_t step(float* S, const void* q, const void* k, const void* v, const fl
 }  // namespace
 
 LinSplit linattn_stream_split(int64_t heads, int64_t max_len, int walks, int D) {
-  // As many blocks as the SMs hold at once by their registers (two rounds of them for d = 128).  The first pass has no queries and no sums over
-  // threads, but it and the chain come on top: cutting gained from four stretches on (one sequence of 8 heads, 4096 tokens,
-  // d = 128, fp32: 489 -> 134 us; 16 heads, 256 tokens, d = 64: 25 -> 16 us; 8 x 32 heads, 2048 tokens, d = 32, bf16:
-  // 266 -> 181 us) and lost with two (4 x 16 heads, 2048 tokens, d = 128: 366 -> 445 us).
+  // As many blocks as the SMs hold at once by their registers (two rounds of them for d = 128).  The first pass has no
+  // queries and no sums over threads, but it and the chain come on top: cutting gained from four stretches on (one
+  // sequence of 8 heads, 4096 tokens, d = 128, fp32: 489 -> 134 us; 16 heads, 256 tokens, d = 64: 25 -> 16 us; 8 x 32
+  // heads, 2048 tokens, d = 32, bf16: 266 -> 181 us) and lost with two (4 x 16 heads, 2048 tokens, d = 128: 366 -> 445 us).
   const int resident = D == 32 ? 7 : D == 64 ? 5 : 4;
   return lin_split(heads * walks * (D / kRows), max_len, 148 * resident, 1, 4);
 }

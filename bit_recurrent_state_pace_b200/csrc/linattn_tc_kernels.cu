@@ -32,8 +32,6 @@
 // Sequences too few to fill the SMs are cut into stretches: the same kernel
 // without outputs gives each stretch's own contribution to the state, a small
 // one chains them, and the stretches then run from their true states.
-#include <type_traits>
-
 #include "linattn_tc.cuh"
 
 namespace pace {
@@ -140,6 +138,7 @@ __device__ __forceinline__ Item item_of(const LinTc& t, const uint16_t* order, i
   if (!it.on) it.c0 = it.c1 = 0;
   return it;
 }
+
 // What an item begins from and leaves: a state of ws, of the walk's tensors (transposed or not), or none.
 struct StateIo {
   bool in, out, in_swap, out_swap;
@@ -189,6 +188,7 @@ __device__ void order_sequences(const LinTc& t, LinSmem<D>& sm) {
     sm.order[rank] = (uint16_t)n;
   }
 }
+
 // ---- loads ---------------------------------------------------------------------
 template <int D, int PARTS, bool STATE_ONLY>
 __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
@@ -506,8 +506,8 @@ __device__ __forceinline__ void value_parts(uint32_t (&v)[PARTS][2][8], uint32_t
 }
 
 // The output of a chunk, the 32 channels of this warp's lanes: OP + weight * OI, in 64 rows of 64 bytes of shared memory
-// whose 16-byte pieces are exchanged as a 64-byte swizzled tensor store wants them.  Sixteen tokens at a time; `read` is called
-// when all accumulators have been read.
+// whose 16-byte pieces are exchanged as a 64-byte swizzled tensor store wants them.  Sixteen tokens at a time; `read` is
+// called when all accumulators have been read.
 template <class F>
 __device__ __forceinline__ void make_out(uint8_t* os, const float* wo, int qd, int lane, F read) {
   const int q = lane & 3, tok = 8 * (lane >> 4) + (lane & 7);       // tok: the row whose address this lane gives
@@ -741,9 +741,9 @@ __device__ __forceinline__ void state_to_tmem(const float (&S)[D / 2], uint32_t 
   ltc::wait_st();
 }
 
-// This thread's part of the state (row e of its half of the key channels) out of shared memory, into it, or exchanged.  Rows of 128
-// bytes whose 16-byte pieces are exchanged by the row's low bits: the lanes of a row-wise access fall in distinct banks,
-// as those of a column-wise one (`swap`: the state lies transposed) do anyway.
+// This thread's part of the state (row e of its half of the key channels) out of shared memory, into it, or exchanged.
+// Rows of 128 bytes whose 16-byte pieces are exchanged by the row's low bits: the lanes of a row-wise access fall in
+// distinct banks, as those of a column-wise one (`swap`: the state lies transposed) do anyway.
 template <int D>
 __device__ __forceinline__ void exchange_state(float (&S)[D / 2], uint8_t* st, int e, bool swap, bool get, bool put) {
   constexpr int HC = D / 2;

@@ -221,7 +221,7 @@ pace_status pace_qk_norm_workspace_bytes(const pace_qk_norm_desc* desc, size_t* 
   if (!bytes) return PACE_ERR_INVALID_ARG;
   const pace_status st = check_norm(desc, &s);
   if (st != PACE_OK) return st;
-  *bytes = pace::qk_norm_partial_bytes(desc->num_tokens, desc->head_dim);
+  *bytes = pace::qk_norm_partial_bytes(desc->head_dim);
   return PACE_OK;
 }
 

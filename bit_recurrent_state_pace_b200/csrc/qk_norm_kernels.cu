@@ -8,8 +8,9 @@
 // number of instructions a row.  A row (one head of one token) is held by L lanes of a warp, 8 elements (one 16-byte load
 // in bf16) each, so a warp's loads are full lines and both sums are shuffles.  A warp takes a token (or, where there are
 // few, a part of one) and goes through its queries, then its keys, U rows a lane at a time with the next ones' loads in
-// flight (asynchronous copies to shared memory: four batches, where registers held one): a lane keeps its columns, so the weights, and the token's cosines and sines, stay in registers.  The angle
-// pos * inv_freq / 2 pi is taken in fp64 and only its fraction goes on in fp32: far positions lose nothing.
+// flight (asynchronous copies to shared memory: four batches, where registers held one): a lane keeps its columns, so the
+// weights, and the token's cosines and sines, stay in registers.  The angle pos * inv_freq / 2 pi is taken in fp64 and
+// only its fraction goes on in fp32: far positions lose nothing.
 //
 // Blocks with one table of angles for their tokens, rows in a flat list, took 174 instructions a row (this: about 80) and
 // waited at a barrier for the table.
@@ -470,7 +471,7 @@ cudaError_t launch_l(const NormArgs& a, cudaStream_t st, int* blocks_out) {
 }
 
 template <bool BF16, bool VEC, int BACK>
-cudaError_t launch_t(const NormArgs& a, int64_t, cudaStream_t st, int* blocks) {
+cudaError_t launch_t(const NormArgs& a, cudaStream_t st, int* blocks) {
   if (VEC) {
     switch (lanes_of(a.D)) {
       case 8: return launch_l<BF16, VEC, 8, BACK>(a, st, blocks);
@@ -482,20 +483,20 @@ cudaError_t launch_t(const NormArgs& a, int64_t, cudaStream_t st, int* blocks) {
 }
 
 template <int BACK>
-cudaError_t launch(const NormArgs& a, int64_t rows, cudaStream_t st, int* blocks) {
+cudaError_t launch(const NormArgs& a, cudaStream_t st, int* blocks) {
   const bool vec = aligned16(a, BACK != 0);
   if (a.io == PACE_IO_BF16)
-    return vec ? launch_t<true, true, BACK>(a, rows, st, blocks) : launch_t<true, false, BACK>(a, rows, st, blocks);
-  return vec ? launch_t<false, true, BACK>(a, rows, st, blocks) : launch_t<false, false, BACK>(a, rows, st, blocks);
+    return vec ? launch_t<true, true, BACK>(a, st, blocks) : launch_t<true, false, BACK>(a, st, blocks);
+  return vec ? launch_t<false, true, BACK>(a, st, blocks) : launch_t<false, false, BACK>(a, st, blocks);
 }
 
 }  // namespace
 
-size_t qk_norm_partial_bytes(int64_t, int D) { return (size_t)kBlocks * 2 * D * sizeof(float); }
+size_t qk_norm_partial_bytes(int D) { return (size_t)kBlocks * 2 * D * sizeof(float); }
 
 cudaError_t launch_qk_norm(const NormArgs& a, cudaStream_t st) {
   const int64_t rows = (int64_t)a.tokens * (a.side[0].heads + a.side[1].heads);
-  return rows == 0 ? cudaSuccess : launch<0>(a, rows, st, nullptr);
+  return rows == 0 ? cudaSuccess : launch<0>(a, st, nullptr);
 }
 
 cudaError_t launch_qk_norm_backward(const NormArgs& a, cudaStream_t st) {
@@ -508,9 +509,9 @@ cudaError_t launch_qk_norm_backward(const NormArgs& a, cudaStream_t st) {
     }
     return cudaSuccess;
   }
-  if (!a.side[0].dw && !a.side[1].dw) return launch<1>(a, rows, st, nullptr);
+  if (!a.side[0].dw && !a.side[1].dw) return launch<1>(a, st, nullptr);
   int blocks = 0;
-  const cudaError_t e = launch<2>(a, rows, st, &blocks);
+  const cudaError_t e = launch<2>(a, st, &blocks);
   if (e != cudaSuccess) return e;
   qk_norm_reduce_kernel<<<dim3((a.D + 31) / 32, 2), 256, 0, st>>>(a.partial, blocks, a.D, a.side[0].dw, a.side[1].dw);
   return cudaGetLastError();

@@ -501,7 +501,8 @@ pace_status pace_linattn_forward(const pace_linattn_desc* desc, const void* q, c
  *   dq_t = S_t^T do_t,  dk_t = D_t^T v_t,  dv_t = D_t k_t,
  *   X_{t-1} = exp(g_h) D_t,   dS0 = X_0  (dS0 NULL: not wanted).
  * dq, dk, dv: io_dtype, in the strides of q, k, v; d_o in that of o.  dS0
- * does not overlap dST or S0.  Bit for bit the same on every call.
+ * does not overlap dST or S0.  Bit for bit the same on every call; in bf16
+ * the last bits of dq, dk and dv may depend on whether dS0 is wanted.
  */
 pace_status pace_linattn_backward(const pace_linattn_desc* desc, const void* q, const void* k, const void* v,
                                   const float* log_decay, const int32_t* cu_seqlens, const float* S0,

@@ -429,6 +429,24 @@ def test_decays_of_every_size(d, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_long_rows_at_odd_addresses(dt):
+    """A long sequence whose rows are aligned to their elements only."""
+    dt, T, H, d = DT[dt], 1300, 1, 64
+    q, k, v, do, S0, dST = make(T, H, d, dt, 1, seed=9)
+    g, cu = torch.tensor([-0.01], device="cuda"), np.array([0, T])
+
+    def odd(x):
+        y = torch.empty(x.numel() + 1, device="cuda", dtype=dt)[1:].view_as(x)
+        return y.copy_(x)
+
+    q1, k1, v1, do1 = (odd(x) for x in (q, k, v, do))
+    o, ST = pace.pace_linattn_forward(q1, k1, v1, g, S0=S0)
+    check_forward(q, k, v, g, S0, cu, o, ST, dt)
+    grads = pace.pace_linattn_backward(q1, k1, v1, g, do1, S0=S0, dST=dST)
+    check_backward(q, k, v, g, S0, do, dST, cu, grads, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_two_graphs_and_an_eager_call(dt):
     """Two captured graphs, replayed in turn with eager calls between them, keep to their own workspaces."""
     dt, T, H, d = DT[dt], 2000, 1, 64

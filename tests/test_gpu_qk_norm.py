@@ -280,3 +280,15 @@ def test_together_as_a_layer_uses_them():
     ot = pace.pace_linattn_step(ST, qt, kt, x[:, 2], g)
     S_want = a * S_before.double().cpu() + x[:, 2].double().cpu()[..., :, None] * kt.double().cpu()[..., None, :]
     assert off(ST, S_want) <= tol and off(ot, (S_want * qt.double().cpu()[..., None, :]).sum(-1)) <= tol
+
+
+def test_numbers_given_as_tensors_are_read_on_every_call():
+    q = make(5, 2, 2, 64, 0, torch.float32, False)[0]
+    scale = torch.tensor(2.0)
+    twice, _ = pace.pace_qk_norm_rotate(q, None, q_scale=scale)
+    scale.fill_(3.0)
+    thrice, _ = pace.pace_qk_norm_rotate(q, None, q_scale=scale)
+    plain = pace.pace_qk_norm_rotate(q, None)[0]
+    # a product of a unit by 2 is exact; by 3 it is rounded where the kernel rounds it
+    assert torch.equal(twice, 2 * plain)
+    assert bool((thrice - 3 * plain).abs().le(4 * ref.U32 * 3 * plain.abs()).all())

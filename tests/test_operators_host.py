@@ -151,3 +151,26 @@ def test_row_strides():
                 torch.zeros(30, 5, 8)):                             # another number of heads
         with pytest.raises(ValueError):
             rows(bad, 4, 8)
+
+
+def test_binding_refuses_what_is_no_tensor_or_integer():
+    q, g = torch.zeros(4, 2, 64), torch.zeros(2)
+    for call in (lambda: pace.pace_linattn_forward(q.numpy(), q, q, g),
+                 lambda: pace.pace_linattn_forward(q, q, q, [0.0, 0.0]),
+                 lambda: pace.pace_linattn_forward(q, q, q, g, num_seqs=2.0),
+                 lambda: pace.pace_linattn_backward(q, q, q, g, q, max_len="4"),
+                 lambda: pace.pace_linattn_step([0], q, q, q, g),
+                 lambda: pace.pace_qk_norm_rotate(q, q, rotary_dim=1.5),
+                 lambda: pace.pace_qk_norm_rotate_backward(q, q, None, None, None, None, 0, q)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_workspace_of_the_walk_in_fp32():
+    """Few heads and long sequences are cut into stretches, whose states lie in the workspace; many heads are not."""
+    size = lambda n, h, d, t, back: pace.pace_linattn_workspace_bytes(n, h, d, pace.PACE_IO_F32, n * t, t, back)  # noqa: E731
+    assert size(1, 1, 64, 64, False) == 0
+    one = size(1, 2, 64, 4096, False)
+    assert one > 0 and one % (2 * 64 * 64 * 4) == 0
+    assert size(64, 32, 64, 4096, False) == size(64, 32, 64, 4096, True) == 0
+    assert size(1, 1, 32, 2 ** 31 - 1, True) > 0
