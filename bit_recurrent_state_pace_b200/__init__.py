@@ -767,9 +767,9 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
             _plain(f"d{name}_weight", dw, (d,), torch.float32, like)
         size = ctypes.c_size_t()
         _check("pace_qk_norm_rotate_backward", lib.pace_qk_norm_workspace_bytes(ctypes.byref(desc), ctypes.byref(size)))
-        return desc, ctypes.byref(desc), (d,), size.value
+        return desc, ctypes.byref(desc), size.value
 
-    _, ref, wide, size = _plan(
+    _, ref, size = _plan(
         ("normb", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq), _form(d_q_out),
          _form(d_k_out), _form(dq), _form(dk), _form(dq_weight), _form(dk_weight), rotary_dim, interleaved, norm, eps,
          q_scale), build)
@@ -779,9 +779,9 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
     if dk is None and k is not None:
         dk = _like(k, stream)
     if dq_weight is None and q is not None and q_weight is not None:
-        dq_weight = _new(wide, torch.float32, like, stream)
+        dq_weight = _like(q_weight, stream)
     if dk_weight is None and k is not None and k_weight is not None:
-        dk_weight = _new(wide, torch.float32, like, stream)
+        dk_weight = _like(k_weight, stream)
     ws = None
     if dq_weight is not None or dk_weight is not None:
         ws = _workspace("pace_qk_norm_rotate_backward", size, workspace, like, stream)
