@@ -23,8 +23,9 @@ constexpr unsigned FULL = 0xffffffffu;
 // (p tokens of decay so far) and reads A^p S query, and the decay of all TT is
 // applied once, in 48 bits -- a product each token would cost half as much
 // again and, by a fixed rounding of A, several 1e-6 of a state that remembers
-// hundreds of tokens.  Heads that forget faster than A^-TT can hold (g < -3)
-// take the product each token.
+// hundreds of tokens.  Heads that forget fast (g < -1) take the product each
+// token: their memory is short, and A^-TT is then below 9e6 for the others, so
+// that it is only for products value key^T above 1e31 that S could overflow.
 //
 // 8 sequences x 16 heads, 1000 tokens, d = 64, fp32: 124 us; 16 x 32 heads, 512 tokens: 177 us, where reads of shared
 // memory and shuffles keep L1 85 % busy (the packed products their pipe 48 %); with fewer heads it is latency.
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kWalkThreads)
   begin += seg * sp.per * kLinChunk;
   const int len = end - begin;
   const float g = clamp_log_decay(a.log_decay[h]), al = expf(g);
-  const bool fast = !(g >= -3.f);
+  const bool fast = !(g >= -1.f);
   if (tid <= TT) {
     const double d = exp((double)g * tid);
     sm.down[tid] = (float)d;

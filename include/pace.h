@@ -461,7 +461,8 @@ pace_status pace_select_head_bits(const double* rates, int32_t num_heads, int32_
  * or one another except where said.
  * A NaN or Inf reaches the outputs that the formulas give it to; in bf16 it
  * may also reach outputs of up to 63 tokens of the same sequence and head
- * before it (behind it, in the gradients for k and v).
+ * before it (behind it, in the gradients for k and v).  Products v k^T (do
+ * q^T) above 1e31 may overflow where the formulas would not.
  */
 typedef struct {
   int32_t num_seqs;          /* N >= 1 */

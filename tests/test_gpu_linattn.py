@@ -429,6 +429,21 @@ def test_decays_of_every_size(d, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [32, 64])
+def test_large_values(d, dt):
+    """Values of 1e30: nothing on the way to finite results overflows, whichever way a head's decay is applied."""
+    dt, T = DT[dt], 70
+    g, cu = torch.tensor([-2.9, -1.001, -0.999, -0.3, -1e-4], device="cuda"), np.array([0, T])
+    q, k, v, do, S0, dST = make(T, 5, d, dt, 1, seed=13)
+    v, S0, do, dST = ((x.float() * 1e30).to(x.dtype) for x in (v, S0, do, dST))
+    o, ST = pace.pace_linattn_forward(q, k, v, g, S0=S0)
+    check_forward(q, k, v, g, S0, cu, o, ST, dt)
+    v, S0 = ((x.float() * 1e-30).to(x.dtype) for x in (v, S0))
+    grads = pace.pace_linattn_backward(q, k, v, g, do, S0=S0, dST=dST)
+    check_backward(q, k, v, g, S0, do, dST, cu, grads, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_long_rows_at_odd_addresses(dt):
     """A long sequence whose rows are aligned to their elements only."""
     dt, T, H, d = DT[dt], 1300, 1, 64
