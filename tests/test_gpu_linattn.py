@@ -444,6 +444,24 @@ def test_large_values(d, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_offsets_beyond_32_bits(dt):
+    """Rows so far apart that the last ones lie more than 2^31 elements behind the first."""
+    dt, T, H, d, far = DT[dt], 140, 1, 64, 1 << 24
+    cu = np.array([0, 65, T])
+    q, k, v, do, S0, dST = make(T, H, d, dt, 2, seed=14)
+    g, dev_cu = torch.tensor([-0.02], device="cuda"), torch.from_numpy(cu.astype(np.int32)).cuda()
+    room = torch.empty(T * far, device="cuda", dtype=dt).view(T, far)
+    parts = [room[:, i * d:(i + 1) * d].unflatten(1, (H, d)) for i in range(8)]
+    for x, y in zip(parts, (q, k, v, do)):
+        x.copy_(y)
+    o, ST = pace.pace_linattn_forward(*parts[:3], g, o=parts[4], cu_seqlens=dev_cu, max_len=75, S0=S0)
+    check_forward(q, k, v, g, S0, cu, o, ST, dt)
+    grads = pace.pace_linattn_backward(*parts[:3], g, parts[3], dq=parts[5], dk=parts[6], dv=parts[7], cu_seqlens=dev_cu,
+                                       max_len=75, S0=S0, dST=dST)
+    check_backward(q, k, v, g, S0, do, dST, cu, grads, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_long_rows_at_odd_addresses(dt):
     """A long sequence whose rows are aligned to their elements only."""
     dt, T, H, d = DT[dt], 1300, 1, 64

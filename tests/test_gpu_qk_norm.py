@@ -292,3 +292,24 @@ def test_numbers_given_as_tensors_are_read_on_every_call():
     # a product of a unit by 2 is exact; by 3 it is rounded where the kernel rounds it
     assert torch.equal(twice, 2 * plain)
     assert bool((thrice - 3 * plain).abs().le(4 * ref.U32 * 3 * plain.abs()).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_offsets_beyond_32_bits(dt):
+    """Rows so far apart that the last ones lie more than 2^31 elements behind the first: what packed rows give."""
+    dt, T, d, far = DT[dt], 140, 64, 1 << 24
+    q, k, wq, wk, pos, inv, dq, dk = make(T, 1, 2, d, d, dt, True)
+    how = dict(rotary_dim=d, norm="rms", eps=EPS)
+    want = pace.pace_qk_norm_rotate(q, k, wq, wk, pos, inv, **how)
+    want_g = pace.pace_qk_norm_rotate_backward(q, k, wq, wk, pos, inv, dq, dk, **how)
+    room = torch.empty(T * far, device="cuda", dtype=dt).view(T, far)
+    parts, at = [], 0
+    for heads in (1, 2, 1, 2):
+        parts.append(room[:, at * d:(at + heads) * d].unflatten(1, (heads, d)))
+        at += heads
+    parts[0].copy_(q)
+    parts[1].copy_(k)
+    got = pace.pace_qk_norm_rotate(parts[0], parts[1], wq, wk, pos, inv, q_out=parts[2], k_out=parts[3], **how)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = pace.pace_qk_norm_rotate_backward(parts[0], parts[1], wq, wk, pos, inv, dq, dk, dq=parts[2], dk=parts[3], **how)
+    assert all(torch.equal(a, b) for a, b in zip(got, want_g))
