@@ -125,7 +125,7 @@ __device__ __forceinline__ void store4(void* p, size_t at, float4 x, bool vec) {
 // `vec`: every row starts on a boundary of four elements, so that four go in one access.  STATE_ONLY: the contribution
 // of each stretch to the state, from zeros into ws.
 template <int D, bool BF16, bool STATE_ONLY>
-__global__ void __launch_bounds__(kWalkThreads)
+__global__ void __launch_bounds__(kWalkThreads, D == 128 ? 1 : 0)      // (d = 128: 155 registers, not 216, 12 % faster)
     linattn_walk_kernel(const __grid_constant__ LinArgs a, const LinSplit sp, float* ws, bool vec) {
   constexpr int CP = D / 32, W = CP < 2 ? 1 : 2;
   constexpr int QKN = TT * D / kWalkThreads / 4;     // pieces of four elements a thread loads
