@@ -34,7 +34,7 @@
 // one chains them, and the stretches then run from their true states.
 //
 // Gradients of 8 x 32 heads, 4096 tokens, d = 128: 887 us (0.32 of the measured copy); 64 prompts of 1 to 1021 tokens, 32
-// heads, with states: 230 us (0.41); one of 65536 tokens, 32 heads: 465 us (0.35).  A chunk takes about 3800 cycles,
+// heads, with states: 235 us (0.40); one of 65536 tokens, 32 heads: 465 us (0.35).  A chunk takes about 3800 cycles,
 // of which its products alone would take 1700; the rest is what the groups wait for one another.  Long runs draw 1000 W,
 // which holds the SM clock at 1.5 to 1.75 GHz.
 #include "linattn_tc.cuh"
