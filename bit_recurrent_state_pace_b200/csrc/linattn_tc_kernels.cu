@@ -734,6 +734,19 @@ __device__ void out_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, in
 }
 
 // ---- state ---------------------------------------------------------------------------
+// What `rows` tokens leave of the state.  Half of it or more: S + m S, m = A^rows - 1, which keeps what a product with
+// A^rows, rounded to 24 bits, would lose chunk after chunk.  Less: the product m S, m = A^rows, off by 2^-24 of what is
+// left, where A^rows - 1, rounded, would be off by 2^-25 of what was there (1 % of what g = -0.2 leaves of a chunk).
+struct Fade {
+  float m;
+  bool rest;
+};
+__device__ __forceinline__ Fade fade_of(float g, int rows) {
+  const float p = g * (float)rows;
+  const bool rest = p > -0.6931f;
+  return {rest ? expm1f(p) : expf(p), rest};
+}
+
 template <int D>
 __device__ __forceinline__ void state_to_tmem(const float (&S)[D / 2], uint32_t at) {
 #pragma unroll
@@ -811,9 +824,8 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
 #pragma unroll
       for (int j = 0; j < HC; ++j) S[j] = 0.f;
     }
-    // A^rows - 1: S + (A^rows - 1) S keeps what a product with A^rows, rounded to 24 bits, would lose chunk after chunk
     const float g = clamp_log_decay(t.a.log_decay[it.h]);
-    const float lost_full = expm1f(g * C), lost_tail = it.chunks() > 0 ? expm1f(g * (float)it.rows(it.c1 - 1)) : 0.f;
+    const Fade full = fade_of(g, C);
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int ch = chunk_at(it, back, c), r = it.rows(ch);
       const uint32_t par = (uint32_t)(k & 1);
@@ -825,13 +837,22 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
         if (lane == 0) tc::mbar_arrive(&sm.s_full);
       }
       if (mine) {        // while U runs
-        const float m = r < C ? lost_tail : lost_full;
-        const float2 m2 = make_float2(m, m);
+        const Fade f = r < C ? fade_of(g, r) : full;
+        const float2 m2 = make_float2(f.m, f.m);
+        if (f.rest) {
 #pragma unroll
-        for (int j = 0; j < HC; j += 2) {
-          const float2 s2 = make_float2(S[j], S[j + 1]), n2 = __ffma2_rn(s2, m2, s2);
-          S[j] = n2.x;
-          S[j + 1] = n2.y;
+          for (int j = 0; j < HC; j += 2) {
+            const float2 s2 = make_float2(S[j], S[j + 1]), n2 = __ffma2_rn(s2, m2, s2);
+            S[j] = n2.x;
+            S[j + 1] = n2.y;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < HC; j += 2) {
+            const float2 n2 = __fmul2_rn(make_float2(S[j], S[j + 1]), m2);
+            S[j] = n2.x;
+            S[j + 1] = n2.y;
+          }
         }
 #pragma unroll
         for (int j = 0; j < HC; ++j) asm volatile("" : "+f"(S[j]));
