@@ -34,7 +34,7 @@ __all__ = [
     "pace_quantize", "pace_dequantize", "pace_pool_status", "pace_pool_clear_status",
     "pace_gdn_step_f32", "pace_gdn_step_bf16", "pace_status_string", "pace_version",
     "PACE_NORM_L2", "PACE_NORM_RMS", "pace_linattn_workspace_bytes", "pace_linattn_forward",
-    "pace_linattn_backward", "pace_linattn_step", "pace_qk_norm_workspace_bytes", "pace_qk_norm_rotate",
+    "pace_linattn_backward", "pace_linattn_step", "pace_debug_linattn_wait", "pace_qk_norm_workspace_bytes", "pace_qk_norm_rotate",
     "pace_qk_norm_rotate_backward",
     "PacePool",
 ]
@@ -123,6 +123,7 @@ def _load():
         "pace_linattn_forward": [ctypes.POINTER(_LinattnDesc)] + [P] * 11,
         "pace_linattn_backward": [ctypes.POINTER(_LinattnDesc)] + [P] * 15,
         "pace_linattn_step": [ctypes.POINTER(_LinattnDesc)] + [P] * 7,
+        "pace_debug_linattn_wait": [ctypes.c_uint32, ctypes.c_uint32],
         "pace_qk_norm_workspace_bytes": [ctypes.POINTER(_QkNormDesc), Sp],
         "pace_qk_norm_rotate": [ctypes.POINTER(_QkNormDesc)] + [P] * 9,
         "pace_qk_norm_rotate_backward": [ctypes.POINTER(_QkNormDesc)] + [P] * 14,
@@ -659,6 +660,10 @@ def pace_linattn_step(S, q, k, v, log_decay, o=None, stream=None) -> torch.Tenso
     _run("pace_linattn_step", lib.pace_linattn_step, q.device.index, stream, ref, S.data_ptr(), q.data_ptr(), k.data_ptr(),
          v.data_ptr(), log_decay.data_ptr(), o.data_ptr())
     return o
+
+
+def pace_debug_linattn_wait(wait_tries: int, extra_tx_bytes: int) -> None:
+    _check("pace_debug_linattn_wait", lib.pace_debug_linattn_wait(int(wait_tries), int(extra_tx_bytes)))
 
 
 _NORM_OF = {"l2": PACE_NORM_L2, "rms": PACE_NORM_RMS, PACE_NORM_L2: PACE_NORM_L2, PACE_NORM_RMS: PACE_NORM_RMS}

@@ -51,19 +51,26 @@ __device__ __forceinline__ void st_16x128b_x4(uint32_t taddr, const uint32_t (&r
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// Wait for phase `parity` of `bar`; false after kWaitTries tests.  The first test is one without a time limit, which
-// costs 52 cycles where the phase is complete (133 with one); a later one suspends the thread for at most 10 us, so that
-// giving up takes 2 s at most and, should no test suspend, still some milliseconds.
+// Wait for phase `parity` of `bar`; false after `tries` tests (kWaitTries, unless a debug limit is set).  The first test is
+// one without a time limit, which costs 52 cycles where the phase is complete (133 with one); a later one suspends the
+// thread for at most 10 us, so that giving up takes 2 s at most and, should no test suspend, still some milliseconds: far
+// above what a chunk takes, which is what a wait of this kernel may last (the one that lasts an item has a budget for each
+// of its chunks).
 constexpr uint32_t kWaitTries = 200000;
-__device__ __forceinline__ bool wait_tries(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_tries(uint64_t* bar, uint32_t parity, uint32_t tries) {
   uint32_t left;
   asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(left)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  if (left) return true;
+  asm volatile(
       "{\n .reg .pred p, z;\n mov.u32 %0, %3;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE_%=;\n"
       "WAIT_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n @p bra DONE_%=;\n"
       " sub.u32 %0, %0, 1;\n setp.ne.u32 z, %0, 0;\n @z bra WAIT_%=;\nDONE_%=:\n}\n"
       : "=&r"(left)
-      : "r"(smem_addr(bar)), "r"(parity), "n"(kWaitTries), "r"(10000u)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(tries), "r"(10000u)
       : "memory");
   return left != 0;
 }
@@ -121,5 +128,6 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 LinSplit linattn_tc_split(int64_t heads, int64_t max_len, int walks);
 bool linattn_tc_takes(const LinArgs& a);
 cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, cudaStream_t st);
+void linattn_tc_debug(uint32_t wait_tries, uint32_t extra_tx);     // 0, 0: the defaults
 
 }  // namespace pace

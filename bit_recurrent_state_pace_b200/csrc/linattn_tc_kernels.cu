@@ -37,6 +37,8 @@
 // heads, with states: 235 us (0.40); one of 65536 tokens, 32 heads: 465 us (0.35).  A chunk takes about 3800 cycles,
 // of which its products alone would take 1700; the rest is what the groups wait for one another.  Long runs draw 1000 W,
 // which holds the SM clock at 1.5 to 1.75 GHz.
+#include <atomic>
+
 #include "linattn_tc.cuh"
 
 namespace pace {
@@ -76,6 +78,8 @@ struct LinTc {
   LinSplit split;
   float* ws;               // [walks][N][H][stretches][D][D]: each stretch's state
   int32_t items;           // (n, h, stretch, walk)
+  uint32_t tries;          // tests of a wait
+  uint32_t extra_tx;       // 0; 16: the first loads' barrier of block 0 waits for more than they bring (debug)
 };
 
 template <int D>
@@ -97,13 +101,16 @@ struct alignas(1024) LinSmem {
   int chunks[kMaxSorted];                                // of each sequence
   uint16_t order[kMaxSorted];                            // sequences, the longest first
   uint32_t taddr;
+  int bad;                                               // a wait gave up
 };
 
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
-  return __all_sync(FULL, ltc::wait_tries(bar, parity)) != 0;
+__device__ __forceinline__ bool wait_all(const LinTc& t, uint64_t* bar, uint32_t parity) {
+  return __all_sync(FULL, ltc::wait_tries(bar, parity, t.tries)) != 0;
 }
-__device__ __forceinline__ void gave_up(uint32_t* flags) {
-  if (flags) atomicOr(flags, PACE_FLAG_TIMEOUT);
+template <int D>
+__device__ __forceinline__ void gave_up(const LinTc& t, LinSmem<D>& sm) {
+  *reinterpret_cast<volatile int*>(&sm.bad) = 1;
+  if (t.a.flags) atomicOr(t.a.flags, PACE_FLAG_TIMEOUT);
 }
 
 // Work item: one walk of one stretch of one sequence and head.
@@ -206,10 +213,10 @@ __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
     const CUtensorMap* mp[3] = {&maps.in[t.map_q[it.w]], &maps.in[t.map_k[it.w]], &maps.in[t.map_v[it.w]]};
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int s = k % NST, r = k / NST;
-      if (r > 0 && !ltc::wait_tries(&sm.empty[s], (uint32_t)((r - 1) & 1))) { ok = false; break; }
+      if (r > 0 && !ltc::wait_tries(&sm.empty[s], (uint32_t)((r - 1) & 1), t.tries)) { ok = false; break; }
       const int row = it.begin + chunk_at(it, back, c) * C;
       constexpr int first = STATE_ONLY ? 1 : 0;
-      mbar_arrive_expect_tx(&sm.full[s], (3 - first) * SM::TILE);
+      mbar_arrive_expect_tx(&sm.full[s], (3 - first) * SM::TILE + (k == 0 && blockIdx.x == 0 ? t.extra_tx : 0u));
 #pragma unroll
       for (int m = first; m < 3; ++m)
 #pragma unroll
@@ -217,11 +224,9 @@ __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
           ltc::tensor_load_2d(smem_addr(&sm.stage[s][m][b * C * 128]), mp[m], it.h * D + 64 * b, row, &sm.full[s]);
     }
   }
-  if (!ok) {
-    gave_up(t.a.flags);
-    // nothing of ours may land after the block has left
-    for (int j = max(0, k - NST); j < k; ++j) ltc::wait_tries(&sm.full[j % NST], (uint32_t)((j / NST) & 1));
-  }
+  if (!ok) gave_up(t, sm);
+  // nothing may land after the block has left, though nobody waits for it
+  for (int j = max(0, k - NST); j < k; ++j) ltc::wait_tries(&sm.full[j % NST], (uint32_t)((j / NST) & 1), t.tries);
 }
 
 // ---- states ---------------------------------------------------------------------
@@ -249,7 +254,12 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
                           &sm.st_full[half]);
   };
   auto done = [&](const Item& it, int half, bool out, bool swap) {
-    if (!ltc::wait_tries(&sm.st_done[half], round[half]++ & 1u)) return false;
+    // the state's warps come to it when they have walked the item: as many budgets as it has chunks, and one
+    const uint32_t par = round[half]++ & 1u;
+    bool there = ltc::wait_tries(&sm.st_done[half], par, t.tries);
+    for (int c = it.chunks(); !there && c > 0 && !*reinterpret_cast<volatile int*>(&sm.bad); --c)
+      there = ltc::wait_tries(&sm.st_done[half], par, t.tries);
+    if (!there) return false;
     if (out) {
       const CUtensorMap* m = STATE_ONLY ? &maps.ws : &maps.s_out[it.w];
       const int row = (STATE_ONLY ? (int)stretch_index(t.a, t.split, it.w, it.n, it.h, it.seg) : it.n * t.a.H + it.h) * D;
@@ -261,7 +271,7 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
     }
     return true;
   };
-  Item last;
+  Item last = {};
   StateIo last_io = {false, false, false, false};
   for (int i = 0; i < item_rounds(t) && ok; ++i) {
     const Item it = item_of<STATE_ONLY>(t, sm.order, i);
@@ -285,10 +295,10 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
     ok = done(last, half, true, last_io.out_swap);
   }
   if (!ok) {
-    gave_up(t.a.flags);
+    gave_up(t, sm);
     // nothing of ours may land after the block has left: a round that gave up had its load before it
     for (int half = 0; half < 2; ++half)
-      if (round[half]) ltc::wait_tries(&sm.st_full[half], (round[half] - 1) & 1u);
+      if (round[half]) ltc::wait_tries(&sm.st_full[half], (round[half] - 1) & 1u, t.tries);
   }
   tc::bulk_wait_all();
 }
@@ -303,10 +313,10 @@ __device__ __forceinline__ int chunks_of_block(const LinTc& t, const LinSmem<D>&
 }
 // every product that the calling warp issued has completed (TMEM is released after that)
 template <int D>
-__device__ __forceinline__ void drain(LinSmem<D>& sm, int which) {
+__device__ __forceinline__ void drain(const LinTc& t, LinSmem<D>& sm, int which) {
   if (ltc::elect_one()) tc::commit(&sm.drain[which]);
   __syncwarp();
-  ltc::wait_tries(&sm.drain[which], 0);
+  ltc::wait_tries(&sm.drain[which], 0, t.tries);
 }
 
 // Warp 1: U of each chunk, as soon as the value's parts are there and the last U has been read.
@@ -322,8 +332,8 @@ __device__ void update_role(const LinTc& t, LinSmem<D>& sm, int total) {
   for (int k = 0; k < total; ++k) {
     const int b = buffer_of<STATE_ONLY>(k);
     const uint32_t par = phase_of<STATE_ONLY>(k);
-    if (!(ok = wait_all(&sm.v_full[b], par))) break;
-    if (used_before<STATE_ONLY>(k) && !(ok = wait_all(&sm.u_empty[b], par ^ 1u))) break;
+    if (!(ok = wait_all(t, &sm.v_full[b], par))) break;
+    if (used_before<STATE_ONLY>(k) && !(ok = wait_all(t, &sm.u_empty[b], par ^ 1u))) break;
     tc::fence_after_sync();
     if (ltc::elect_one()) {
 #pragma unroll 1
@@ -337,8 +347,8 @@ __device__ void update_role(const LinTc& t, LinSmem<D>& sm, int total) {
     __syncwarp();
     s = s + 1 == NST ? 0 : s + 1;
   }
-  if (!ok) gave_up(t.a.flags);
-  drain<D>(sm, 0);
+  if (!ok) gave_up(t, sm);
+  drain<D>(t, sm, 0);
 }
 
 // Warp 3: SC of the next chunk as soon as this one's has been read, then this one's OI and OP.
@@ -368,7 +378,7 @@ __device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
   };
   bool ok = true;
   if (total > 0) {
-    ok = wait_all(&sm.full[0], 0);
+    ok = wait_all(t, &sm.full[0], 0);
     if (ok) scores(0);
   }
   int s = 0, turn = 0;                       // stage of chunk k and how often the stages went round
@@ -376,14 +386,14 @@ __device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
     const uint32_t par = (uint32_t)(k & 1);
     const int sn = s + 1 == NST ? 0 : s + 1, turn_n = s + 1 == NST ? turn + 1 : turn;
     if (k + 1 < total) {
-      if (!(ok = wait_all(&sm.sc_empty, par))) break;
-      if (!(ok = wait_all(&sm.full[sn], (uint32_t)(turn_n & 1)))) break;
+      if (!(ok = wait_all(t, &sm.sc_empty, par))) break;
+      if (!(ok = wait_all(t, &sm.full[sn], (uint32_t)(turn_n & 1)))) break;
       tc::fence_after_sync();
       scores(sn);
     }
     // the state before the chunk is in TMEM, and the last chunk's output has been read
-    if (!(ok = wait_all(&sm.s_full, par))) break;
-    if (k > 0 && !(ok = wait_all(&sm.o_empty, par ^ 1u))) break;
+    if (!(ok = wait_all(t, &sm.s_full, par))) break;
+    if (k > 0 && !(ok = wait_all(t, &sm.o_empty, par ^ 1u))) break;
     tc::fence_after_sync();
     if (ltc::elect_one()) {
 #pragma unroll 1
@@ -394,7 +404,7 @@ __device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
     }
     __syncwarp();
     // P of this chunk, and zeros in its values behind the sequence's end
-    if (!(ok = wait_all(&sm.p_full, par))) break;
+    if (!(ok = wait_all(t, &sm.p_full, par))) break;
     tc::fence_after_sync();
     if (ltc::elect_one()) {
 #pragma unroll 1
@@ -409,8 +419,8 @@ __device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
     s = sn;
     turn = turn_n;
   }
-  if (!ok) gave_up(t.a.flags);
-  drain<D>(sm, 1);
+  if (!ok) gave_up(t, sm);
+  drain<D>(t, sm, 1);
 }
 
 // ---- P, the value's parts, the output -------------------------------------------------
@@ -598,7 +608,7 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     if (tc::named_sync_any(1 + th, 128, !ok)) break;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int r = it.rows(chunk_at(it, back, c));
-      if (!(ok = wait_all(&sm.full[s], turn))) break;
+      if (!(ok = wait_all(t, &sm.full[s], turn))) break;
       uint32_t v[PARTS][2][8];
       if (32 * qd < D) value_parts<PARTS>(v, smem_addr(sm.stage[s][2]), wv[r < C], r, th, qd, lane);
       if (r < C) {
@@ -608,7 +618,7 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       }
       const int b = buffer_of<STATE_ONLY>(k);
       // the parts that were there have been used
-      if (used_before<STATE_ONLY>(k) && !(ok = wait_all(&sm.u_full[b], phase_of<STATE_ONLY>(k) ^ 1u))) break;
+      if (used_before<STATE_ONLY>(k) && !(ok = wait_all(t, &sm.u_full[b], phase_of<STATE_ONLY>(k) ^ 1u))) break;
       tc::fence_after_sync();
       if (32 * qd < D) {
 #pragma unroll
@@ -632,7 +642,7 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       }
     }
   }
-  if (!ok) gave_up(t.a.flags);
+  if (!ok) gave_up(t, sm);
 }
 
 // Warps 12-15: P from the scores.
@@ -651,7 +661,7 @@ __device__ void score_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     if (tid < 8) pz[2 * C + tid] = 0.f;
     if (tc::named_sync_any(3, 128, !ok)) break;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
-      if (!(ok = wait_all(&sm.sc_full, (uint32_t)(k & 1)))) break;
+      if (!(ok = wait_all(t, &sm.sc_full, (uint32_t)(k & 1)))) break;
       tc::fence_after_sync();
       uint32_t x[32];
       tc::ld_16x256b_x8(((uint32_t)(32 * qd) << 16) + T_SC, x);
@@ -662,7 +672,7 @@ __device__ void score_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       const int r = it.rows(chunk_at(it, back, c));
       if (r < C) zero_rows<D>(sm.stage[k % NST][2], r, tid, 128);      // values behind the sequence's end, as the keys
       make_p(x, pz + C, back ? -1 : 1, r, qd, lane);
-      if (k > 0 && !(ok = wait_all(&sm.op_full, (uint32_t)((k - 1) & 1)))) break;     // the last P has been used
+      if (k > 0 && !(ok = wait_all(t, &sm.op_full, (uint32_t)((k - 1) & 1)))) break;     // the last P has been used
       tc::fence_after_sync();
       // matrices: (rows 0-7, block y), (rows 8-15, block y), (rows 0-7, block y + 1), (rows 8-15, block y + 1)
       const uint32_t row = 16 * qd + (lane & 15), to = smem_addr(sm.p) + row * 128;
@@ -678,7 +688,7 @@ __device__ void score_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       if (lane == 0) tc::mbar_arrive(&sm.p_full);
     }
   }
-  if (!ok) gave_up(t.a.flags);
+  if (!ok) gave_up(t, sm);
 }
 
 // Warps 16-19: the outputs.
@@ -699,7 +709,7 @@ __device__ void out_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, in
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int ch = chunk_at(it, w.back, c), r = it.rows(ch), row = it.begin + ch * C;
       if (lane == 0) tc::bulk_wait_read_all();     // the last tile's store has left the buffer
-      if (!(ok = wait_all(&sm.op_full, (uint32_t)(k & 1)))) break;
+      if (!(ok = wait_all(t, &sm.op_full, (uint32_t)(k & 1)))) break;
       tc::fence_after_sync();
       auto read = [&] {
         tc::fence_before_sync();
@@ -730,7 +740,7 @@ __device__ void out_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, in
     }
   }
   if (lane == 0) tc::bulk_wait_all();
-  if (!ok) gave_up(t.a.flags);
+  if (!ok) gave_up(t, sm);
 }
 
 // ---- state ---------------------------------------------------------------------------
@@ -801,7 +811,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   float S[HC];
   StateIo last_io = {false, false, false, false};
   auto exchange = [&](bool swap, bool get, bool put) {
-    if (!wait_all(&sm.st_full[half], round++ & 1u)) return false;
+    if (!wait_all(t, &sm.st_full[half], round++ & 1u)) return false;
     if (mine) exchange_state<D>(S, sm.st, e, swap, get, put);
     fence_proxy_async_smem();
     __syncwarp();
@@ -857,7 +867,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
 #pragma unroll
         for (int j = 0; j < HC; ++j) asm volatile("" : "+f"(S[j]));
       }
-      if (!(ok = wait_all(&sm.u_full[buffer_of<STATE_ONLY>(k)], phase_of<STATE_ONLY>(k)))) break;
+      if (!(ok = wait_all(t, &sm.u_full[buffer_of<STATE_ONLY>(k)], phase_of<STATE_ONLY>(k)))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int j0 = 0; j0 < HC; j0 += 16) {
@@ -882,7 +892,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
         }
       }
       if (STATE_ONLY) continue;
-      if (!(ok = wait_all(&sm.op_full, par))) break;          // the last copy has been used
+      if (!(ok = wait_all(t, &sm.op_full, par))) break;          // the last copy has been used
       tc::fence_after_sync();
       if (c + 1 < it.chunks()) {
         if (mine) state_to_tmem<D>(S, lane_addr + T_S + (HC / 2) * half);
@@ -894,7 +904,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     if (!ok) break;
   }
   if (ok && last_io.out) ok = exchange(last_io.out_swap, false, true);
-  if (!ok) gave_up(t.a.flags);
+  if (!ok) gave_up(t, sm);
 }
 
 template <int D, int PARTS, bool STATE_ONLY>
@@ -926,6 +936,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&sm.drain[0], 1);
     mbar_init(&sm.drain[1], 1);
     mbar_init(&sm.sc_empty, 4);
+    sm.bad = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(&sm.taddr, 512);
@@ -1051,8 +1062,16 @@ bool linattn_tc_takes(const LinArgs& a) {
   return true;
 }
 
+static std::atomic<uint32_t> g_wait_tries{ltc::kWaitTries}, g_extra_tx{0};
+void linattn_tc_debug(uint32_t wait_tries, uint32_t extra_tx) {
+  g_wait_tries = wait_tries ? wait_tries : ltc::kWaitTries;
+  g_extra_tx = extra_tx;
+}
+
 cudaError_t launch_linattn_tc(const LinArgs& a, const LinSplit& sp, float* ws, cudaStream_t st) {
   LinTc t;
+  t.tries = g_wait_tries;
+  t.extra_tx = g_extra_tx;
   LinMaps maps;
   t.a = a;
   t.split = sp;

@@ -192,6 +192,18 @@ pace_status pace_linattn_backward(const pace_linattn_desc* desc, const void* q, 
   return run_walks(desc, a, d_workspace, as_stream(stream));
 }
 
+pace_status pace_debug_linattn_wait(uint32_t wait_tries, uint32_t extra_tx_bytes) {
+  if (wait_tries == 0 && extra_tx_bytes == 0) {
+    pace::linattn_tc_debug(0, 0);
+    return PACE_OK;
+  }
+  if (wait_tries < 100 || wait_tries > pace::ltc::kWaitTries || (extra_tx_bytes != 0 && extra_tx_bytes != 16))
+    return PACE_ERR_INVALID_ARG;
+  if (extra_tx_bytes && wait_tries > 1000) return PACE_ERR_INVALID_ARG;
+  pace::linattn_tc_debug(wait_tries, extra_tx_bytes);
+  return PACE_OK;
+}
+
 pace_status pace_linattn_step(const pace_linattn_desc* desc, float* S, const void* q, const void* k, const void* v,
                               const float* log_decay, void* o, void* stream) {
   LinShape s;

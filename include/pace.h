@@ -519,6 +519,20 @@ pace_status pace_linattn_step(const pace_linattn_desc* desc, float* S, const voi
                               const float* log_decay, void* o, void* stream);
 
 /*
+ * Debug only: the bounded waits of the bf16 prompts and gradients above (d =
+ * 64 and 128), as pace_debug_wait_fault does for the decode.
+ *  wait_tries:      tests of one wait before it gives up, 100 .. 200000 (the
+ *    default); a test lasts 10 us at most.
+ *  extra_tx_bytes:  0 or 16.  With 16 (wait_tries <= 1000) the first barrier
+ *    of the first block expects 16 bytes more than its copies bring: every
+ *    copy still lands, the barrier never completes, and the block gives up.
+ * (0, 0) restores the defaults.  Out-of-range values are
+ * PACE_ERR_INVALID_ARG and change nothing.  Host-only; applies to every call
+ * of this process enqueued (or captured) after it.
+ */
+pace_status pace_debug_linattn_wait(uint32_t wait_tries, uint32_t extra_tx_bytes);
+
+/*
  * Queries and keys, normalised for each head and turned by their position in
  * one pass: what pace_decode_step, pace_prefill and the linear attention
  * above take as q and k.  For a row x of one head (d elements):
