@@ -907,6 +907,30 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   if (!ok) gave_up(t, sm);
 }
 
+// A block in which a wait gave up leaves NaN in all that its items were to write, so that nobody takes what lies there for
+// results (a stretch's state hands them on to the stretches behind it).  Threads 0 .. 255 of the state's warps, when every
+// store of the block has completed.
+template <int D, bool STATE_ONLY>
+__device__ void spoil(const LinTc& t, const LinSmem<D>& sm, int thread) {
+  for (int i = 0; i < item_rounds(t); ++i) {
+    const Item it = item_of<STATE_ONLY>(t, sm.order, i);
+    if (!it.on) continue;
+    const LinWalk& w = t.a.walk[it.w];
+    if (!STATE_ONLY) {
+      const int r0 = it.begin + it.c0 * C, rows = min(it.len - it.c0 * C, (it.c1 - it.c0) * C);
+      for (int64_t x = thread; x < (int64_t)rows * (D / 8); x += 256) {
+        uint16_t* dst = reinterpret_cast<uint16_t*>(w.out) + (r0 + x / (D / 8)) * w.out_stride + it.h * D + 8 * (x % (D / 8));
+        *reinterpret_cast<uint4*>(dst) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+      }
+    }
+    if (state_io<STATE_ONLY>(t, it).out) {
+      float* S = STATE_ONLY ? t.ws + stretch_index(t.a, t.split, it.w, it.n, it.h, it.seg) * (D * D)
+                            : w.S_out + ((int64_t)it.n * t.a.H + it.h) * (D * D);
+      for (int x = thread; x < D * D; x += 256) S[x] = __int_as_float(0x7fffffff);
+    }
+  }
+}
+
 template <int D, int PARTS, bool STATE_ONLY>
 __global__ void __launch_bounds__(kTcThreads, 1)
     linattn_tc_kernel(const __grid_constant__ LinTc t, const __grid_constant__ LinMaps maps) {
@@ -958,17 +982,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (!STATE_ONLY) {
       output_mma_role<D>(t, sm, chunks_of_block<D, STATE_ONLY>(t, sm));
     }
+    tc::named_sync(5, kTcThreads);
   } else if (warp < 12) {
     value_role<D, PARTS, STATE_ONLY>(t, sm, warp, lane);
+    tc::named_sync(5, kTcThreads);
   } else if (warp < 16) {
     ltc::regs_down<64>();
     if (!STATE_ONLY) score_role<D>(t, sm, warp, lane);
+    tc::named_sync(5, kTcThreads);
   } else if (warp < 20) {
     ltc::regs_down<48>();
     if (!STATE_ONLY) out_role<D>(t, maps, sm, warp, lane);
+    tc::named_sync(5, kTcThreads);
   } else {
     ltc::regs_up<104>();
     state_role<D, PARTS, STATE_ONLY>(t, sm, warp, lane);
+    tc::named_sync(5, kTcThreads);           // every role is through, its stores completed
+    if (*reinterpret_cast<volatile int*>(&sm.bad)) spoil<D, STATE_ONLY>(t, sm, tid - 640);
   }
   tc::fence_before_sync();
   __syncthreads();

@@ -488,8 +488,9 @@ pace_status pace_linattn_workspace_bytes(const pace_linattn_desc* desc, int32_t 
  * used by anything else until the work on `stream` is done (two graphs that
  * may run side by side need one each); NULL where 0 bytes are needed.
  * d_flags: optional device uint32; receives PACE_FLAG_TIMEOUT by atomic OR
- * if a bounded wait inside a kernel gave up.  Enqueues only, allocates
- * nothing; may be captured into a graph.
+ * if a bounded wait inside a kernel gave up; the outputs and states that it
+ * was to write are NaN then, with d_flags or without.  Enqueues only,
+ * allocates nothing; may be captured into a graph.
  */
 pace_status pace_linattn_forward(const pace_linattn_desc* desc, const void* q, const void* k, const void* v,
                                  const float* log_decay, const int32_t* cu_seqlens, const float* S0, void* o,
@@ -525,7 +526,8 @@ pace_status pace_linattn_step(const pace_linattn_desc* desc, float* S, const voi
  *    default); a test lasts 10 us at most.
  *  extra_tx_bytes:  0 or 16.  With 16 (wait_tries <= 1000) the first barrier
  *    of the first block expects 16 bytes more than its copies bring: every
- *    copy still lands, the barrier never completes, and the block gives up.
+ *    copy still lands, the barrier never completes, and the block gives up:
+ *    its outputs are NaN and PACE_FLAG_TIMEOUT is set.
  * (0, 0) restores the defaults.  Out-of-range values are
  * PACE_ERR_INVALID_ARG and change nothing.  Host-only; applies to every call
  * of this process enqueued (or captured) after it.

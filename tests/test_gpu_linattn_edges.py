@@ -60,3 +60,57 @@ def test_a_wait_is_bounded_by_its_work(d, waits):
     got, flags = both()
     assert flags == 0
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def calls(T, H, d, n, seed):
+    q, k, v, do, S0, dST = make(n * T, H, d, torch.bfloat16, n, seed=seed)
+    g = torch.full((H,), -0.05, device="cuda")
+
+    def both(flags=None):
+        """(o, ST) and (dq, dk, dv, dS0)"""
+        return (pace.pace_linattn_forward(q, k, v, g, num_seqs=n, S0=S0, flags=flags),
+                pace.pace_linattn_backward(q, k, v, g, do, num_seqs=n, S0=S0, dST=dST, flags=flags))
+
+    return both
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 64, 200, 4000])
+def test_a_wait_that_runs_out_is_seen(T, d, waits):
+    """The first barrier never completes: the launch ends, sets the flag, and leaves NaN where its results were to be, with
+    a flag word or without; the calls after it are right.  (4000 tokens are cut into stretches.)"""
+    both = calls(T, 1, d, 1, 23)
+    want = both()
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    waits(100, 16)
+    a.record()
+    (o, ST), (dq, dk, dv, dS0) = both(flags)
+    b.record()
+    torch.cuda.synchronize()
+    assert int(flags) == pace.PACE_FLAG_TIMEOUT
+    assert a.elapsed_time(b) < 200.0                         # not the default limit of 2 s a wait
+    # the first block of a backward pass walks for dv and dS0, of cut sequences over the first rows
+    for x in (o, ST, dv[:200], dS0):
+        assert bool(torch.isnan(x).all())
+    (o, ST), (_, _, dv, dS0) = both()
+    assert all(bool(torch.isnan(x).all()) for x in (o, ST, dv[:200], dS0))
+    waits(0, 0)
+    flags.zero_()
+    got = both(flags)
+    assert int(flags) == 0
+    assert all(torch.equal(x, y) for w, r in zip(want, got) for x, y in zip(w, r))
+
+
+def test_a_wait_that_runs_out_is_one_blocks(waits):
+    """200 sequences of one head on 148 blocks: the first block's two sequences are NaN, the others what they were."""
+    n, T, d = 200, 70, 128
+    (o, ST), _ = want = calls(T, 1, d, n, 24)()
+    waits(100, 16)
+    (o2, ST2), _ = calls(T, 1, d, n, 24)()
+    lost = torch.zeros(n, dtype=torch.bool, device="cuda")
+    lost[[0, 148]] = True
+    o, o2 = o.view(n, T, d), o2.view(n, T, d)
+    assert torch.equal(o[~lost], o2[~lost]) and torch.equal(ST[~lost], ST2[~lost])
+    assert bool(torch.isnan(o2[lost]).all()) and bool(torch.isnan(ST2[lost]).all())
