@@ -66,6 +66,55 @@ pace::LinArgs lin_args(const pace_linattn_desc* d, const float* log_decay, const
   return a;
 }
 
+// A tensor's bytes: `rows` of `width`, `stride` apart (width <= stride where there are several).
+struct Bytes {
+  const void* p;
+  int64_t width, stride, rows;
+};
+inline Bytes io_bytes(const void* p, int64_t elements, int64_t stride, int64_t rows, size_t esz) {
+  return Bytes{p, elements * (int64_t)esz, stride * (int64_t)esz, rows};
+}
+inline Bytes state_bytes(const float* p, const pace_linattn_desc* d) {
+  const int64_t n = (int64_t)d->num_seqs * d->num_heads * d->d_k * d->d_v * 4;
+  return Bytes{p, n, n, 1};
+}
+inline Bytes vector_bytes(const float* p, int n) { return Bytes{p, 4 * (int64_t)n, 4 * (int64_t)n, 1}; }
+
+// Whether a byte of row i of a, at i stride, is one of row j of b: -width_b < (b - a) + t stride < width_a for a t = j - i.
+bool rows_meet(const Bytes& a, const Bytes& b, int64_t stride) {
+  const __int128 at = (__int128)(intptr_t)b.p - (intptr_t)a.p;
+  auto floor_div = [&](__int128 x) { return x >= 0 ? x / stride : -((-x + stride - 1) / stride); };
+  __int128 low = floor_div(-b.width - at) + 1, high = floor_div(a.width - 1 - at);
+  if (low < 1 - (__int128)a.rows) low = 1 - (__int128)a.rows;
+  if (high > b.rows - 1) high = b.rows - 1;
+  return low <= high;
+}
+// Whether two tensors share memory: exact for rows at one stride (parts of one wider row do not, where their columns
+// differ) or where one of them is a single row; of rows at two strides only the first ones are looked for in the other
+// tensor.
+bool overlap(const Bytes& a, const Bytes& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  auto behind = [](const Bytes& x) { return (__int128)(intptr_t)x.p + (__int128)(x.rows - 1) * x.stride + x.width; };
+  if (behind(a) <= (intptr_t)b.p || behind(b) <= (intptr_t)a.p) return false;
+  if (a.rows == 1 || a.stride == b.stride) return rows_meet(a, b, b.stride);
+  if (b.rows == 1) return rows_meet(a, b, a.stride);
+  Bytes a0 = a, b0 = b;
+  a0.rows = b0.rows = 1;
+  return rows_meet(a0, b, b.stride) || rows_meet(a, b0, a.stride);
+}
+// Outputs do not overlap inputs or one another: rows of a head or sequence are read by several blocks, in any order.
+bool apart(const Bytes* outs, int n_out, const Bytes* ins, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(outs[i], ins[j])) return false;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return false;
+  }
+  return true;
+}
+// ... or are the very input, row for row
+inline bool same_rows(const Bytes& a, const Bytes& b) { return a.p == b.p && (a.stride == b.stride || a.rows <= 1); }
+
 // Walks over all sequences, on the tensor cores where their shapes allow.  The workspace depends on the desc alone: where
 // alignment keeps a shape that the tensor cores would take off them, the sequences are not cut.
 inline bool tc_shape(const pace_linattn_desc* d) { return d->io_dtype == PACE_IO_BF16 && d->d_k >= 64; }
@@ -162,6 +211,11 @@ pace_status pace_linattn_forward(const pace_linattn_desc* desc, const void* q, c
   if (!log_decay || !aligned(log_decay, 4) || !aligned(cu_seqlens, 4) || !state_ok(S0) || !state_ok(ST) ||
       !aligned(d_flags, 4) || !aligned(d_workspace, 256))
     return PACE_ERR_INVALID_ARG;
+  const int64_t w = (int64_t)desc->num_heads * desc->d_k, rows = desc->total_tokens;
+  const Bytes outs[2] = {io_bytes(o, w, s.os, rows, s.esz), state_bytes(ST, desc)};
+  const Bytes ins[4] = {io_bytes(q, w, s.qs, rows, s.esz), io_bytes(k, w, s.ks, rows, s.esz), io_bytes(v, w, s.vs, rows, s.esz),
+                        state_bytes(ST == S0 ? nullptr : S0, desc)};
+  if (!apart(outs, 2, ins, 4)) return PACE_ERR_INVALID_ARG;
   pace::LinArgs a = lin_args(desc, log_decay, cu_seqlens, d_flags);
   a.walks = 1;
   a.walk[0] = pace::LinWalk{q, k, v, o, s.qs, s.ks, s.vs, s.os, S0, ST, 0, 0};
@@ -183,7 +237,12 @@ pace_status pace_linattn_backward(const pace_linattn_desc* desc, const void* q, 
   if (!log_decay || !aligned(log_decay, 4) || !aligned(cu_seqlens, 4) || !state_ok(S0) || !state_ok(dST) ||
       !state_ok(dS0) || !aligned(d_flags, 4) || !aligned(d_workspace, 256))
     return PACE_ERR_INVALID_ARG;
-  if (dS0 && (dS0 == dST || dS0 == S0)) return PACE_ERR_INVALID_ARG;
+  const int64_t w = (int64_t)desc->num_heads * desc->d_k, rows = desc->total_tokens;
+  const Bytes outs[4] = {io_bytes(dq, w, s.qs, rows, s.esz), io_bytes(dk, w, s.ks, rows, s.esz),
+                         io_bytes(dv, w, s.vs, rows, s.esz), state_bytes(dS0, desc)};
+  const Bytes ins[6] = {io_bytes(q, w, s.qs, rows, s.esz), io_bytes(k, w, s.ks, rows, s.esz), io_bytes(v, w, s.vs, rows, s.esz),
+                        io_bytes(d_o, w, s.os, rows, s.esz), state_bytes(S0, desc), state_bytes(dST, desc)};
+  if (!apart(outs, 4, ins, 6)) return PACE_ERR_INVALID_ARG;
   pace::LinArgs a = lin_args(desc, log_decay, cu_seqlens, d_flags);
   a.walks = 3;
   a.walk[0] = pace::LinWalk{k, q, d_o, dv, s.ks, s.qs, s.os, s.vs, dST, dS0, 1, 0};
@@ -212,6 +271,10 @@ pace_status pace_linattn_step(const pace_linattn_desc* desc, float* S, const voi
   if (!S || !state_ok(S) || !log_decay || !aligned(log_decay, 4) || !io_ok(q, s.esz, true) || !io_ok(k, s.esz, true) ||
       !io_ok(v, s.esz, true) || !io_ok(o, s.esz, true))
     return PACE_ERR_INVALID_ARG;
+  const int64_t w = (int64_t)desc->num_heads * desc->d_k, rows = desc->num_seqs;
+  const Bytes outs[2] = {io_bytes(o, w, s.os, rows, s.esz), state_bytes(S, desc)};
+  const Bytes ins[3] = {io_bytes(q, w, s.qs, rows, s.esz), io_bytes(k, w, s.ks, rows, s.esz), io_bytes(v, w, s.vs, rows, s.esz)};
+  if (!apart(outs, 2, ins, 3)) return PACE_ERR_INVALID_ARG;
   return from_cuda(pace::launch_linattn_step(S, q, k, v, log_decay, o, s.qs, s.ks, s.vs, s.os, desc->num_seqs,
                                              desc->num_heads, desc->d_k, desc->io_dtype, as_stream(stream)));
 }
@@ -224,7 +287,13 @@ pace_status pace_qk_norm_rotate(const pace_qk_norm_desc* desc, const void* q, co
   pace_status st = check_norm(desc, &s);
   if (st == PACE_OK) st = norm_args(desc, s, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, &a);
   if (st != PACE_OK) return st;
-  if ((q && q_out == q && s.qs != s.qo) || (k && k_out == k && s.ks != s.ko)) return PACE_ERR_INVALID_ARG;
+  const int64_t wq = (int64_t)desc->num_q_heads * desc->head_dim, wk = (int64_t)desc->num_k_heads * desc->head_dim;
+  const int64_t rows = desc->num_tokens;
+  const Bytes outs[2] = {io_bytes(q_out, wq, s.qo, rows, s.esz), io_bytes(k_out, wk, s.ko, rows, s.esz)};
+  const Bytes ins[2] = {io_bytes(q, wq, s.qs, rows, s.esz), io_bytes(k, wk, s.ks, rows, s.esz)};
+  for (int i = 0; i < 2; ++i)
+    if ((overlap(outs[i], ins[i]) && !same_rows(outs[i], ins[i])) || overlap(outs[i], ins[1 - i])) return PACE_ERR_INVALID_ARG;
+  if (overlap(outs[0], outs[1])) return PACE_ERR_INVALID_ARG;
   return from_cuda(pace::launch_qk_norm(a, as_stream(stream)));
 }
 
@@ -251,8 +320,17 @@ pace_status pace_qk_norm_rotate_backward(const pace_qk_norm_desc* desc, const vo
   if (!io_ok(d_q_out, s.esz, any && desc->num_q_heads) || !io_ok(d_k_out, s.esz, any && desc->num_k_heads))
     return PACE_ERR_INVALID_ARG;
   const int64_t wq = (int64_t)desc->num_q_heads * desc->head_dim, wk = (int64_t)desc->num_k_heads * desc->head_dim;
-  if ((d_q_out && dq == d_q_out && s.qo != wq) || (d_k_out && dk == d_k_out && s.ko != wk)) return PACE_ERR_INVALID_ARG;
-  if ((q && dq == q && s.qo != s.qs) || (k && dk == k && s.ko != s.ks)) return PACE_ERR_INVALID_ARG;
+  const int64_t rows = desc->num_tokens;
+  const Bytes outs[2] = {io_bytes(dq, wq, s.qo, rows, s.esz), io_bytes(dk, wk, s.ko, rows, s.esz)};
+  const Bytes ins[2] = {io_bytes(q, wq, s.qs, rows, s.esz), io_bytes(k, wk, s.ks, rows, s.esz)};
+  const Bytes grads[2] = {io_bytes(d_q_out, wq, wq, rows, s.esz), io_bytes(d_k_out, wk, wk, rows, s.esz)};
+  for (int i = 0; i < 2; ++i) {
+    if (overlap(outs[i], ins[1 - i]) || overlap(outs[i], grads[1 - i])) return PACE_ERR_INVALID_ARG;
+    if (overlap(outs[i], ins[i]) && !same_rows(outs[i], ins[i])) return PACE_ERR_INVALID_ARG;
+    if (overlap(outs[i], grads[i]) && !same_rows(outs[i], grads[i])) return PACE_ERR_INVALID_ARG;
+  }
+  if (overlap(outs[0], outs[1])) return PACE_ERR_INVALID_ARG;
+  if (overlap(vector_bytes(dq_weight, desc->head_dim), vector_bytes(dk_weight, desc->head_dim))) return PACE_ERR_INVALID_ARG;
   if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return PACE_ERR_INVALID_ARG;
   if ((dq_weight || dk_weight) && (!d_workspace || !aligned(d_workspace, 256))) return PACE_ERR_INVALID_ARG;
   a.side[0].dy = d_q_out;

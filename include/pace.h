@@ -458,7 +458,9 @@ pace_status pace_select_head_bits(const double* rates, int32_t num_heads, int32_
  * <= 0, -inf: no memory.
  * States: device fp32 [num_seqs][num_heads][d_v][d_k], 16-byte aligned.
  * io tensors are aligned to the element size.  Outputs do not overlap inputs
- * or one another except where said.
+ * or one another except where said: rows at one stride that do, and states
+ * that do, are refused (parts of one wider row do not, where their columns
+ * differ).
  * A NaN or Inf reaches the outputs that the formulas give it to; in bf16 it
  * may also reach outputs of up to 63 tokens of the same sequence and head
  * before it (behind it, in the gradients for k and v).  Products v k^T (do
@@ -552,7 +554,8 @@ pace_status pace_debug_linattn_wait(uint32_t wait_tries, uint32_t extra_tx_bytes
  * as in pace_linattn_desc; q_weight, k_weight: device fp32 [d] or NULL;
  * positions: device int32 [num_tokens], inv_freq: device fp32
  * [rotary_dim / 2] (both NULL where rotary_dim is 0).  q_out may be q and
- * k_out may be k (with equal strides).  Sums of squares are fp32: rows whose
+ * k_out may be k (with equal strides); they overlap no other input nor one
+ * another, as above.  Sums of squares are fp32: rows whose
  * sum overflows give zeros, as the formula in fp32 does.
  */
 typedef enum { PACE_NORM_L2 = 0, PACE_NORM_RMS = 1 } pace_norm_kind;
