@@ -460,6 +460,14 @@ def _whole(name: str, x) -> Optional[int]:
         raise ValueError(f"{name}: an integer, not {type(x).__name__}") from None
 
 
+def _number(name: str, x) -> float:
+    """A real number as a float."""
+    try:
+        return float(x)
+    except (TypeError, ValueError, RuntimeError):
+        raise ValueError(f"{name}: a number, not {type(x).__name__}") from None
+
+
 def _form(t):
     if t is None:
         return None
@@ -502,7 +510,8 @@ def _like(t: torch.Tensor, stream) -> torch.Tensor:
 def _workspace(name: str, nbytes: int, given: Optional[torch.Tensor], like: torch.Tensor, stream):
     if given is None:
         return _new(nbytes, torch.uint8, like, stream) if nbytes else None
-    _need(given.is_cuda and given.device == like.device and given.is_contiguous(), f"{name}: workspace on {like.device}")
+    _need(isinstance(given, torch.Tensor) and given.is_cuda and given.device == like.device and given.is_contiguous(),
+          f"{name}: workspace: a contiguous tensor on {like.device}")
     _need(given.numel() * given.element_size() >= nbytes, f"{name}: workspace of {nbytes} bytes")
     return given
 
@@ -512,6 +521,7 @@ def _linattn(q, k, v, log_decay, num_seqs, max_len, cu_seqlens):
     _need(isinstance(q, torch.Tensor) and q.is_cuda, "libpace takes device tensors")
     _need(q.dtype in _IO_OF, f"q: bfloat16 or float32, not {q.dtype}")
     _need(q.dim() in (3, 4), "q: [tokens, heads, d] or [sequences, tokens, heads, d]")
+    _need(log_decay is not None, "log_decay: the heads' log decays")
     H, d = q.shape[-2], q.shape[-1]
     total, qs = _rows("q", q, H, d, q)
     tk, ks = _rows("k", k, H, d, q)
@@ -648,7 +658,7 @@ def pace_linattn_step(S, q, k, v, log_decay, o=None, stream=None) -> torch.Tenso
             rows, st = (n, 0) if name == "o" and t is None else _rows(name, t, H, d, q)
             _need(rows == n, f"{name}: {n} rows")
             strides.append(st)
-        _need(S is not None, "S: the states")
+        _need(S is not None and log_decay is not None, "S and log_decay: the states and the heads' log decays")
         _plain("S", S, (n, H, d, d), torch.float32, q)
         _plain("log_decay", log_decay, (H,), torch.float32, q)
         desc = _LinattnDesc(n, H, d, d, _IO_OF[q.dtype], 0, 0, *strides)
@@ -669,12 +679,18 @@ def pace_debug_linattn_wait(wait_tries: int, extra_tx_bytes: int) -> None:
 _NORM_OF = {"l2": PACE_NORM_L2, "rms": PACE_NORM_RMS, PACE_NORM_L2: PACE_NORM_L2, PACE_NORM_RMS: PACE_NORM_RMS}
 
 
+def _norm_kind(norm) -> int:
+    try:
+        return _NORM_OF[norm]
+    except (KeyError, TypeError):                # TypeError: nothing that can be looked up
+        raise ValueError(f"norm: 'l2' or 'rms', not {norm!r}") from None
+
+
 def _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interleaved, norm, eps, q_scale):
     """Descriptor (strides of q and k set), the tensor that gives type and device, heads, rows and d."""
     like = q if q is not None else k
     _need(isinstance(like, torch.Tensor) and like.dim() >= 3, "q or k: device tensor [..., heads, d]")
     _need(like.dtype in _IO_OF, f"q, k: bfloat16 or float32, not {like.dtype}")
-    _need(norm in _NORM_OF, "norm: 'l2' or 'rms'")
     d = like.shape[-1]
     heads, rows, strides = [0, 0], [], [0, 0]
     for i, (name, t) in enumerate((("q", q), ("k", k))):
@@ -693,7 +709,7 @@ def _qk_norm(q, k, q_weight, k_weight, positions, inv_freq, rotary_dim, interlea
     _plain("k_weight", k_weight, (d,), torch.float32, like)
     _plain("positions", positions, () if positions is None else positions.shape, torch.int32, like)
     _plain("inv_freq", inv_freq, (half,), torch.float32, like)
-    desc = _QkNormDesc(rows[0], heads[0], heads[1], d, int(rotary_dim), int(bool(interleaved)), _NORM_OF[norm],
+    desc = _QkNormDesc(rows[0], heads[0], heads[1], d, int(rotary_dim), int(bool(interleaved)), norm,
                        _IO_OF[like.dtype], float(eps), float(q_scale), strides[0], strides[1], 0, 0)
     return desc, like, heads, rows[0], d
 
@@ -704,7 +720,8 @@ def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_
 
     q: [tokens, Hq, d], k: [tokens, Hk, d] (either may be None); q_out may be q, k_out may be k.
     """
-    rotary_dim, interleaved, eps, q_scale = _whole("rotary_dim", rotary_dim) or 0, bool(interleaved), float(eps), float(q_scale)
+    rotary_dim, interleaved, norm = _whole("rotary_dim", rotary_dim) or 0, bool(interleaved), _norm_kind(norm)
+    eps, q_scale = _number("eps", eps), _number("q_scale", q_scale)
 
     def build():
         _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),
@@ -746,7 +763,8 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
                                  q_scale=1.0, workspace=None, stream=None):
     """Gradients of pace_qk_norm_rotate: returns (dq, dk, dq_weight, dk_weight); a weight's gradient is made where the
     weight is given (or a tensor for it)."""
-    rotary_dim, interleaved, eps, q_scale = _whole("rotary_dim", rotary_dim) or 0, bool(interleaved), float(eps), float(q_scale)
+    rotary_dim, interleaved, norm = _whole("rotary_dim", rotary_dim) or 0, bool(interleaved), _norm_kind(norm)
+    eps, q_scale = _number("eps", eps), _number("q_scale", q_scale)
 
     def build():
         _tensors(("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("positions", positions),

@@ -114,3 +114,14 @@ def test_a_wait_that_runs_out_is_one_blocks(waits):
     o, o2 = o.view(n, T, d), o2.view(n, T, d)
     assert torch.equal(o[~lost], o2[~lost]) and torch.equal(ST[~lost], ST2[~lost])
     assert bool(torch.isnan(o2[lost]).all()) and bool(torch.isnan(ST2[lost]).all())
+
+
+def test_what_is_missing_is_refused():
+    q, k, v, do, S0, _ = make(8, 2, 64, torch.bfloat16, 8)
+    for call in (lambda: pace.pace_linattn_forward(q, k, v, None),
+                 lambda: pace.pace_linattn_backward(q, k, v, None, do),
+                 lambda: pace.pace_linattn_step(S0, q, k, v, None),
+                 lambda: pace.pace_linattn_step(None, q, k, v, torch.zeros(2, device="cuda")),
+                 lambda: pace.pace_linattn_forward(q, k, v, torch.zeros(2, device="cuda"), workspace=0)):
+        with pytest.raises(ValueError):
+            call()

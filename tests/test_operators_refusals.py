@@ -3,6 +3,7 @@ anything is launched."""
 import ctypes
 
 import pytest
+import torch
 
 import bit_recurrent_state_pace_b200 as pace
 
@@ -85,3 +86,17 @@ def test_norm_outputs_over_other_inputs():
     assert bwd(qo, qo + 64) == 1 and bwd(qo, q) == 1 and bwd(qo, dyq) == 1
     assert bwd(dyq, ko, q_out_stride=512) == 1
     assert bwd(qo, ko, w, w) == 1 and bwd(qo, ko, w, w + 252) == 1
+
+
+def test_the_binding_refuses_with_value_errors():
+    q = torch.zeros(4, 2, 64)
+    for name, call in (("norm", lambda: pace.pace_qk_norm_rotate(q, q, norm=["l2"])),
+                       ("norm", lambda: pace.pace_qk_norm_rotate(q, q, norm={})),
+                       ("norm", lambda: pace.pace_qk_norm_rotate_backward(q, q, None, None, None, None, q, q, norm=2)),
+                       ("eps", lambda: pace.pace_qk_norm_rotate(q, q, eps=None)),
+                       ("q_scale", lambda: pace.pace_qk_norm_rotate(q, q, q_scale="one")),
+                       ("q_scale", lambda: pace.pace_qk_norm_rotate(q, q, q_scale=torch.ones(2)))):
+        with pytest.raises(ValueError, match=name):
+            call()
+    with pytest.raises(ValueError, match="workspace"):
+        pace._workspace("call", 256, [0], q, None)
