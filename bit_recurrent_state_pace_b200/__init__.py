@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import operator
 import os
+import warnings
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -363,7 +364,9 @@ def pace_gdn_step_bf16(S, q, k, v, alpha, beta, io, o, n, d_k, d_v, stream=None)
 # These calls check shapes, types and devices (the C entry points see pointers
 # only), run on the device of their first tensor whichever device is current,
 # allocate the outputs and the workspace that are not given, and return the
-# outputs.  Token rows may lie apart (a part of a wider projection): the last
+# outputs, which are detached: autograd records nothing (a warning says so where
+# an input requires gradients; the _backward calls are for autograd functions).
+# Token rows may lie apart (a part of a wider projection): the last
 # two dimensions are dense, the row stride is free.
 
 _IO_OF = {torch.bfloat16: PACE_IO_BF16, torch.float32: PACE_IO_F32}
@@ -487,6 +490,16 @@ def _plan(key, build):
     return plan
 
 
+def _detached(name: str, *tensors) -> None:
+    """Says so where autograd would be expected to record the call: the outputs are detached."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                warnings.warn(f"{name} records nothing for autograd, its outputs are detached from inputs that require gradients: "
+                              f"call it in an autograd function (or under torch.no_grad())", stacklevel=3)
+                return
+
+
 def _opt(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -588,6 +601,7 @@ def pace_linattn_forward(q, k, v, log_decay, o=None, ST=None, num_seqs=None, max
 
     desc, ref, states, size = _plan(("fwd", _form(q), _form(k), _form(v), _form(log_decay), _form(o), _form(ST),
                                      _form(cu_seqlens), _form(S0), _form(flags), num_seqs, max_len), build)
+    _detached("pace_linattn_forward", q, k, v, log_decay, S0)
     if o is None:
         o = _like(q, stream)
     if ST is None and need_ST:
@@ -629,6 +643,7 @@ def pace_linattn_backward(q, k, v, log_decay, d_o, dq=None, dk=None, dv=None, dS
     desc, ref, states, rooms, size = _plan(
         ("bwd", _form(q), _form(k), _form(v), _form(log_decay), _form(d_o), _form(dq), _form(dk), _form(dv), _form(dS0),
          _form(cu_seqlens), _form(S0), _form(dST), _form(flags), num_seqs, max_len), build)
+    _detached("pace_linattn_backward", q, k, v, log_decay, S0, d_o, dST)
     made = []
     for given, like, room in ((dq, q, rooms[0]), (dk, k, rooms[1]), (dv, v, rooms[2])):
         if given is None:
@@ -665,6 +680,7 @@ def pace_linattn_step(S, q, k, v, log_decay, o=None, stream=None) -> torch.Tenso
         return desc, ctypes.byref(desc)
 
     _, ref = _plan(("step", _form(S), _form(q), _form(k), _form(v), _form(log_decay), _form(o)), build)
+    _detached("pace_linattn_step", S, q, k, v, log_decay)
     if o is None:
         o = _like(q, stream)
     _run("pace_linattn_step", lib.pace_linattn_step, q.device.index, stream, ref, S.data_ptr(), q.data_ptr(), k.data_ptr(),
@@ -742,6 +758,7 @@ def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_
 
     _, ref = _plan(("norm", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq),
                     _form(q_out), _form(k_out), rotary_dim, interleaved, norm, eps, q_scale), build)
+    _detached("pace_qk_norm_rotate", q, k, q_weight, k_weight)
     if q_out is None and q is not None:
         q_out = _like(q, stream)
     if k_out is None and k is not None:
@@ -796,6 +813,7 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
         ("normb", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq), _form(d_q_out),
          _form(d_k_out), _form(dq), _form(dk), _form(dq_weight), _form(dk_weight), rotary_dim, interleaved, norm, eps,
          q_scale), build)
+    _detached("pace_qk_norm_rotate_backward", q, k, q_weight, k_weight, d_q_out, d_k_out)
     like = q if q is not None else k
     if dq is None and q is not None:
         dq = _like(q, stream)

@@ -1,4 +1,6 @@
 """Edges of the linear attention with a fixed decay for each head: large states that fade, waits, refusals, NaN."""
+import warnings
+
 import numpy as np
 import pytest
 import torch
@@ -125,3 +127,32 @@ def test_what_is_missing_is_refused():
                  lambda: pace.pace_linattn_forward(q, k, v, torch.zeros(2, device="cuda"), workspace=0)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_detached_outputs_are_announced():
+    """Nothing is recorded for autograd: a call that would be expected to is told so, one in an autograd function or
+    without gradients is not, and the values are the same."""
+    q, k, v, do, S0, _ = make(8, 2, 64, torch.float32, 8)
+    g, w = torch.tensor([-0.1, -0.2], device="cuda"), torch.ones(64, device="cuda")
+    want = pace.pace_linattn_forward(q, k, v, g, S0=S0[:1])[0]
+
+    def all_of():
+        return [lambda: pace.pace_linattn_forward(q, k, v, g, S0=S0[:1])[0],
+                lambda: pace.pace_linattn_backward(q, k, v, g, do, S0=S0[:1])[0],
+                lambda: pace.pace_linattn_step(S0.clone(), q, k, v, g),
+                lambda: pace.pace_qk_norm_rotate(q, k, w, w)[0],
+                lambda: pace.pace_qk_norm_rotate_backward(q, k, w, w, None, None, do, do)[0]]
+
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        for call in all_of():
+            call()
+        q.requires_grad_()
+        with torch.no_grad():
+            for call in all_of():
+                call()
+    for call in all_of():
+        with pytest.warns(UserWarning, match="detached"):
+            assert not call().requires_grad
+    with pytest.warns(UserWarning):
+        assert torch.equal(want, pace.pace_linattn_forward(q, k, v, g, S0=S0[:1])[0])
