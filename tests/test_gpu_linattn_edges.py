@@ -156,3 +156,54 @@ def test_detached_outputs_are_announced():
             assert not call().requires_grad
     with pytest.warns(UserWarning):
         assert torch.equal(want, pace.pace_linattn_forward(q, k, v, g, S0=S0[:1])[0])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")], ids=str)
+def test_what_is_not_a_number_stays_causal(what, d, dt):
+    """A NaN or infinity at token t, in one channel or all of them, reaches the outputs from t on (gradients for k and v: up
+    to t) and none that the formulas keep from it, which come out bit for bit as without it.  (bf16 with d = 64 and 128:
+    but for the other tokens of its 64, counted from the sequence's first one.)"""
+    dt, H, T = DT[dt], 2, 150
+    cu, dev_cu = lengths(70, 80)
+    base = dict(zip(("q", "k", "v", "do"), make(T, H, d, dt, 2, seed=31)[:4]))
+    S0, dST = make(T, H, d, dt, 2, seed=32)[4:]
+    g = torch.tensor([-0.02, -0.3], device="cuda")
+
+    def run(x, states):
+        s = dict(S0=S0) if states else {}
+        o, ST = pace.pace_linattn_forward(x["q"], x["k"], x["v"], g, cu_seqlens=dev_cu, max_len=80, **s)
+        if states:
+            s["dST"] = dST
+        dq, dk, dv, _ = pace.pace_linattn_backward(x["q"], x["k"], x["v"], g, x["do"], cu_seqlens=dev_cu, max_len=80, **s)
+        return dict(o=o, dq=dq, dk=dk, dv=dv)
+
+    # which outputs an input reaches: from it on, up to it, at it alone
+    on, upto, at = "on", "upto", "at"
+    reach = dict(q=dict(o=at, dk=upto, dv=upto), k=dict(o=on, dq=on, dv=at), v=dict(o=on, dq=on, dk=at),
+                 do=dict(dq=at, dk=upto, dv=upto))
+    for states in (True, False):
+        want = run(base, states)
+        for name in reach:
+            for t in (0, 5, 31, 63, 64, 69, 70, 100, 133, 134, 149):
+                b, e = (0, 70) if t < 70 else (70, 150)
+                for channels in (slice(None), slice(d - 3, d - 2)):
+                    x = dict(base, **{name: base[name].clone()})
+                    x[name][t, 1, channels] = what
+                    got = run(x, states)
+                    for out, y in got.items():
+                        hit = torch.zeros(T, H, dtype=torch.bool, device="cuda")
+                        kind = reach[name].get(out)
+                        first, last = t, t + 1
+                        if dt == torch.bfloat16 and d > 32:
+                            first = b + (t - b) // 64 * 64
+                            last = min(first + 64, e)
+                        if kind == on:
+                            hit[first:e, 1] = True
+                        elif kind == upto:
+                            hit[b:last, 1] = True
+                        elif kind == at:
+                            hit[t, 1] = True
+                        assert torch.equal(y[~hit], want[out][~hit]), (name, t, out, kind)
+                        assert kind is None or not bool(torch.isfinite(y[t, 1]).all()), (name, t, out, kind)
