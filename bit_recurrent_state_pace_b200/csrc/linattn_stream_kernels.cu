@@ -379,12 +379,20 @@ cudaError_t step(float* S, const void* q, const void* k, const void* v, const fl
 }  // namespace
 
 LinSplit linattn_stream_split(int64_t heads, int64_t max_len, int walks, int D) {
-  // As many blocks as the SMs hold at once by their registers (two rounds of them for d = 128).  The first pass has no
-  // queries and no sums over threads, but it and the chain come on top: cutting gained from four stretches on (one
-  // sequence of 8 heads, 4096 tokens, d = 128, fp32: 489 -> 134 us; 16 heads, 256 tokens, d = 64: 25 -> 16 us; 8 x 32
-  // heads, 2048 tokens, d = 32, bf16: 266 -> 181 us) and lost with two (4 x 16 heads, 2048 tokens, d = 128: 366 -> 445 us).
-  const int resident = D == 32 ? 7 : D == 64 ? 5 : 4;
-  return lin_split(heads * walks * (D / kRows), max_len, 148 * resident, 1, 4);
+  // The first pass has no queries and no sums over threads, but it and the chain come on top.
+  const int64_t items = heads * walks * (D / kRows);
+  if (D == 128) {
+    // Three rounds of the 3 blocks an SM holds, so that the last one's idle SMs weigh little, but a sequence in no more than
+    // 148 stretches (the chain).  fp32, us, against one and a third rounds, as before / one round / uncut: 8 heads x 4096
+    // tokens 129 / 142 / 128 / 486, their gradients 324 / 341 / 368 / 488; 48 heads 611 / 716 / 668 / 716; 16 heads x 1024
+    // tokens 73 / 78 / 82 / 126.  It gained with 192 blocks (those 48 heads) and lost from 220 on (55 heads x 2048 tokens: 361
+    // uncut, 371 cut; 4 x 16 heads: 361, 407; gradients of 32 heads x 4096 tokens: 973, 1150).
+    const int64_t fill = 148 * (items < 9 ? items : 9);
+    return lin_split(items, max_len, items <= 200 ? fill : 0, 1, 4);
+  }
+  // As many blocks as the SMs hold at once by their registers.  Cutting gained from four stretches on (16 heads, 256 tokens,
+  // d = 64: 25 -> 16 us; 8 x 32 heads, 2048 tokens, d = 32, bf16: 266 -> 181 us).
+  return lin_split(items, max_len, 148 * (D == 32 ? 7 : 5), 1, 4);
 }
 
 cudaError_t launch_linattn_stream(const LinArgs& a, const LinSplit& sp, float* ws, cudaStream_t st) {
