@@ -202,7 +202,7 @@ __device__ void order_sequences(const LinTc& t, LinSmem<D>& sm) {
 }
 
 // ---- loads ---------------------------------------------------------------------
-template <int D, int PARTS, bool STATE_ONLY>
+template <int D, bool STATE_ONLY>
 __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
   using SM = LinSmem<D>;
   int k = 0;
@@ -235,7 +235,7 @@ __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
 // goes out.  The next item's first half is there long before its use.  Each round: (load or not) -> st_full -> the
 // exchange -> st_done -> (store or not).  By the state's own threads, row by row, reading and writing a state took
 // 14,000 cycles of an item.
-template <int D, int PARTS, bool STATE_ONLY>
+template <int D, bool STATE_ONLY>
 __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
   uint32_t round[2] = {0, 0};
   bool ok = true;
@@ -265,7 +265,7 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
       const int row = (STATE_ONLY ? (int)stretch_index(t.a, t.split, it.w, it.n, it.h, it.seg) : it.n * t.a.H + it.h) * D;
       const int boxes = swap ? D / 32 : D / 64, bytes = swap ? D * 64 : D * 128;
       for (int b = 0; b < boxes; ++b)
-        ltc::tensor_store_2d(m, smem_addr(sm.st) + b * bytes, 32 * b + (swap ? 0 : D / 2 * half), row + (swap ? D / 2 * half : 0));
+        tc::tensor_store_2d(m, smem_addr(sm.st) + b * bytes, 32 * b + (swap ? 0 : D / 2 * half), row + (swap ? D / 2 * half : 0));
       tc::bulk_commit_group();
       tc::bulk_wait_read_all();
     }
@@ -725,7 +725,7 @@ __device__ void out_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, in
       __syncwarp();
       if (r == C) {
         if (lane == 0) {
-          ltc::tensor_store_2d(&maps.out[it.w], smem_addr(os), it.h * D + 32 * qd, row);
+          tc::tensor_store_2d(&maps.out[it.w], smem_addr(os), it.h * D + 32 * qd, row);
           tc::bulk_commit_group();
         }
       } else {
@@ -799,7 +799,7 @@ __device__ __forceinline__ void exchange_state(float (&S)[D / 2], uint8_t* st, i
   }
 }
 
-template <int D, int PARTS, bool STATE_ONLY>
+template <int D, bool STATE_ONLY>
 __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   constexpr int HC = D / 2;                                  // key channels of a thread
   const int qd = warp & 3, half = (warp - 20) >> 2, e = 32 * qd + lane;
@@ -972,12 +972,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp < 4) {
     ltc::regs_down<40>();
     if (warp == 0) {
-      if (lane == 0) load_role<D, PARTS, STATE_ONLY>(t, maps, sm);
+      if (lane == 0) load_role<D, STATE_ONLY>(t, maps, sm);
       __syncwarp();
     } else if (warp == 1) {
       update_role<D, PARTS, STATE_ONLY>(t, sm, chunks_of_block<D, STATE_ONLY>(t, sm));
     } else if (warp == 2) {
-      if (lane == 0) state_io_role<D, PARTS, STATE_ONLY>(t, maps, sm);
+      if (lane == 0) state_io_role<D, STATE_ONLY>(t, maps, sm);
       __syncwarp();
     } else if (!STATE_ONLY) {
       output_mma_role<D>(t, sm, chunks_of_block<D, STATE_ONLY>(t, sm));
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc::named_sync(5, kTcThreads);
   } else {
     ltc::regs_up<104>();
-    state_role<D, PARTS, STATE_ONLY>(t, sm, warp, lane);
+    state_role<D, STATE_ONLY>(t, sm, warp, lane);
     tc::named_sync(5, kTcThreads);           // every role is through, its stores completed
     if (*reinterpret_cast<volatile int*>(&sm.bad)) spoil<D, STATE_ONLY>(t, sm, tid - 640);
   }

@@ -113,8 +113,8 @@ __device__ __forceinline__ void bulk_store(void* gdst, uint32_t ssrc, uint32_t b
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(ssrc), "r"(bytes)
                : "memory");
 }
-// 2-D tiled store of a box at coordinates (x, y); x * element size must be a
-// multiple of 16 bytes (here x = 0).
+// 2-D tiled store of a box at coordinates (x, y), neither negative; x * element
+// size must be a multiple of 16 bytes.
 __device__ __forceinline__ void tensor_store_2d(const CUtensorMap* map, uint32_t ssrc, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
                "r"(ssrc), "r"(x), "r"(y)
