@@ -51,26 +51,24 @@ __device__ __forceinline__ void st_16x128b_x4(uint32_t taddr, const uint32_t (&r
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// Wait for phase `parity` of `bar`; false after `tries` tests (kWaitTries, unless a debug limit is set).  The first test is
+// Wait for phase `parity` of `bar`; false after kWaitTries tests (or the debug limit).  The first test is
 // one without a time limit, which costs 52 cycles where the phase is complete (133 with one); a later one suspends the
 // thread for at most 10 us, so that giving up takes 2 s at most and, should no test suspend, still some milliseconds: far
 // above what a chunk takes, which is what a wait of this kernel may last (the one that lasts an item has a budget for each
 // of its chunks).
 constexpr uint32_t kWaitTries = 200000;
-__device__ __forceinline__ bool wait_tries(uint64_t* bar, uint32_t parity, uint32_t tries) {
+// sm.tries: that number, in shared memory, so that a phase that is complete costs no more than its test.
+template <class SM>
+__device__ __forceinline__ bool wait_tries(const SM& sm, uint64_t* bar, uint32_t parity) {
   uint32_t left;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(left)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  if (left) return true;
-  asm volatile(
-      "{\n .reg .pred p, z;\n mov.u32 %0, %3;\n"
-      "WAIT_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n @p bra DONE_%=;\n"
+      "{\n .reg .pred p, z;\n mov.u32 %0, 1;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE_%=;\n"
+      " ld.shared.u32 %0, [%3+%4];\n"
+      "WAIT_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %5;\n @p bra DONE_%=;\n"
       " sub.u32 %0, %0, 1;\n setp.ne.u32 z, %0, 0;\n @z bra WAIT_%=;\nDONE_%=:\n}\n"
       : "=&r"(left)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(tries), "r"(10000u)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(smem_addr(&sm)), "n"(offsetof(SM, tries)), "r"(10000u)
       : "memory");
   return left != 0;
 }

@@ -102,10 +102,12 @@ struct alignas(1024) LinSmem {
   uint16_t order[kMaxSorted];                            // sequences, the longest first
   uint32_t taddr;
   int bad;                                               // a wait gave up
+  uint32_t tries;                                        // tests of a wait
 };
 
-__device__ __forceinline__ bool wait_all(const LinTc& t, uint64_t* bar, uint32_t parity) {
-  return __all_sync(FULL, ltc::wait_tries(bar, parity, t.tries)) != 0;
+template <class SM>
+__device__ __forceinline__ bool wait_all(const SM& sm, uint64_t* bar, uint32_t parity) {
+  return __all_sync(FULL, ltc::wait_tries(sm, bar, parity)) != 0;
 }
 template <int D>
 __device__ __forceinline__ void gave_up(const LinTc& t, LinSmem<D>& sm) {
@@ -213,7 +215,7 @@ __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
     const CUtensorMap* mp[3] = {&maps.in[t.map_q[it.w]], &maps.in[t.map_k[it.w]], &maps.in[t.map_v[it.w]]};
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int s = k % NST, r = k / NST;
-      if (r > 0 && !ltc::wait_tries(&sm.empty[s], (uint32_t)((r - 1) & 1), t.tries)) { ok = false; break; }
+      if (r > 0 && !ltc::wait_tries(sm, &sm.empty[s], (uint32_t)((r - 1) & 1))) { ok = false; break; }
       const int row = it.begin + chunk_at(it, back, c) * C;
       constexpr int first = STATE_ONLY ? 1 : 0;
       mbar_arrive_expect_tx(&sm.full[s], (3 - first) * SM::TILE + (k == 0 && blockIdx.x == 0 ? t.extra_tx : 0u));
@@ -226,7 +228,7 @@ __device__ void load_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm) {
   }
   if (!ok) gave_up(t, sm);
   // nothing may land after the block has left, though nobody waits for it
-  for (int j = max(0, k - NST); j < k; ++j) ltc::wait_tries(&sm.full[j % NST], (uint32_t)((j / NST) & 1), t.tries);
+  for (int j = max(0, k - NST); j < k; ++j) ltc::wait_tries(sm, &sm.full[j % NST], (uint32_t)((j / NST) & 1));
 }
 
 // ---- states ---------------------------------------------------------------------
@@ -256,9 +258,9 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
   auto done = [&](const Item& it, int half, bool out, bool swap) {
     // the state's warps come to it when they have walked the item: as many budgets as it has chunks, and one
     const uint32_t par = round[half]++ & 1u;
-    bool there = ltc::wait_tries(&sm.st_done[half], par, t.tries);
+    bool there = ltc::wait_tries(sm, &sm.st_done[half], par);
     for (int c = it.chunks(); !there && c > 0 && !*reinterpret_cast<volatile int*>(&sm.bad); --c)
-      there = ltc::wait_tries(&sm.st_done[half], par, t.tries);
+      there = ltc::wait_tries(sm, &sm.st_done[half], par);
     if (!there) return false;
     if (out) {
       const CUtensorMap* m = STATE_ONLY ? &maps.ws : &maps.s_out[it.w];
@@ -298,7 +300,7 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
     gave_up(t, sm);
     // nothing of ours may land after the block has left: a round that gave up had its load before it
     for (int half = 0; half < 2; ++half)
-      if (round[half]) ltc::wait_tries(&sm.st_full[half], (round[half] - 1) & 1u, t.tries);
+      if (round[half]) ltc::wait_tries(sm, &sm.st_full[half], (round[half] - 1) & 1u);
   }
   tc::bulk_wait_all();
 }
@@ -313,10 +315,10 @@ __device__ __forceinline__ int chunks_of_block(const LinTc& t, const LinSmem<D>&
 }
 // every product that the calling warp issued has completed (TMEM is released after that)
 template <int D>
-__device__ __forceinline__ void drain(const LinTc& t, LinSmem<D>& sm, int which) {
+__device__ __forceinline__ void drain(LinSmem<D>& sm, int which) {
   if (ltc::elect_one()) tc::commit(&sm.drain[which]);
   __syncwarp();
-  ltc::wait_tries(&sm.drain[which], 0, t.tries);
+  ltc::wait_tries(sm, &sm.drain[which], 0);
 }
 
 // Warp 1: U of each chunk, as soon as the value's parts are there and the last U has been read.
@@ -332,8 +334,8 @@ __device__ void update_role(const LinTc& t, LinSmem<D>& sm, int total) {
   for (int k = 0; k < total; ++k) {
     const int b = buffer_of<STATE_ONLY>(k);
     const uint32_t par = phase_of<STATE_ONLY>(k);
-    if (!(ok = wait_all(t, &sm.v_full[b], par))) break;
-    if (used_before<STATE_ONLY>(k) && !(ok = wait_all(t, &sm.u_empty[b], par ^ 1u))) break;
+    if (!(ok = wait_all(sm, &sm.v_full[b], par))) break;
+    if (used_before<STATE_ONLY>(k) && !(ok = wait_all(sm, &sm.u_empty[b], par ^ 1u))) break;
     tc::fence_after_sync();
     if (ltc::elect_one()) {
 #pragma unroll 1
@@ -348,7 +350,7 @@ __device__ void update_role(const LinTc& t, LinSmem<D>& sm, int total) {
     s = s + 1 == NST ? 0 : s + 1;
   }
   if (!ok) gave_up(t, sm);
-  drain<D>(t, sm, 0);
+  drain<D>(sm, 0);
 }
 
 // Warp 3: SC of the next chunk as soon as this one's has been read, then this one's OI and OP.
@@ -378,7 +380,7 @@ __device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
   };
   bool ok = true;
   if (total > 0) {
-    ok = wait_all(t, &sm.full[0], 0);
+    ok = wait_all(sm, &sm.full[0], 0);
     if (ok) scores(0);
   }
   int s = 0, turn = 0;                       // stage of chunk k and how often the stages went round
@@ -386,14 +388,14 @@ __device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
     const uint32_t par = (uint32_t)(k & 1);
     const int sn = s + 1 == NST ? 0 : s + 1, turn_n = s + 1 == NST ? turn + 1 : turn;
     if (k + 1 < total) {
-      if (!(ok = wait_all(t, &sm.sc_empty, par))) break;
-      if (!(ok = wait_all(t, &sm.full[sn], (uint32_t)(turn_n & 1)))) break;
+      if (!(ok = wait_all(sm, &sm.sc_empty, par))) break;
+      if (!(ok = wait_all(sm, &sm.full[sn], (uint32_t)(turn_n & 1)))) break;
       tc::fence_after_sync();
       scores(sn);
     }
     // the state before the chunk is in TMEM, and the last chunk's output has been read
-    if (!(ok = wait_all(t, &sm.s_full, par))) break;
-    if (k > 0 && !(ok = wait_all(t, &sm.o_empty, par ^ 1u))) break;
+    if (!(ok = wait_all(sm, &sm.s_full, par))) break;
+    if (k > 0 && !(ok = wait_all(sm, &sm.o_empty, par ^ 1u))) break;
     tc::fence_after_sync();
     if (ltc::elect_one()) {
 #pragma unroll 1
@@ -404,7 +406,7 @@ __device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
     }
     __syncwarp();
     // P of this chunk, and zeros in its values behind the sequence's end
-    if (!(ok = wait_all(t, &sm.p_full, par))) break;
+    if (!(ok = wait_all(sm, &sm.p_full, par))) break;
     tc::fence_after_sync();
     if (ltc::elect_one()) {
 #pragma unroll 1
@@ -420,7 +422,7 @@ __device__ void output_mma_role(const LinTc& t, LinSmem<D>& sm, int total) {
     turn = turn_n;
   }
   if (!ok) gave_up(t, sm);
-  drain<D>(t, sm, 1);
+  drain<D>(sm, 1);
 }
 
 // ---- P, the value's parts, the output -------------------------------------------------
@@ -608,7 +610,7 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     if (tc::named_sync_any(1 + th, 128, !ok)) break;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int r = it.rows(chunk_at(it, back, c));
-      if (!(ok = wait_all(t, &sm.full[s], turn))) break;
+      if (!(ok = wait_all(sm, &sm.full[s], turn))) break;
       uint32_t v[PARTS][2][8];
       if (32 * qd < D) value_parts<PARTS>(v, smem_addr(sm.stage[s][2]), wv[r < C], r, th, qd, lane);
       if (r < C) {
@@ -618,7 +620,7 @@ __device__ void value_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       }
       const int b = buffer_of<STATE_ONLY>(k);
       // the parts that were there have been used
-      if (used_before<STATE_ONLY>(k) && !(ok = wait_all(t, &sm.u_full[b], phase_of<STATE_ONLY>(k) ^ 1u))) break;
+      if (used_before<STATE_ONLY>(k) && !(ok = wait_all(sm, &sm.u_full[b], phase_of<STATE_ONLY>(k) ^ 1u))) break;
       tc::fence_after_sync();
       if (32 * qd < D) {
 #pragma unroll
@@ -661,7 +663,7 @@ __device__ void score_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     if (tid < 8) pz[2 * C + tid] = 0.f;
     if (tc::named_sync_any(3, 128, !ok)) break;
     for (int c = 0; c < it.chunks(); ++c, ++k) {
-      if (!(ok = wait_all(t, &sm.sc_full, (uint32_t)(k & 1)))) break;
+      if (!(ok = wait_all(sm, &sm.sc_full, (uint32_t)(k & 1)))) break;
       tc::fence_after_sync();
       uint32_t x[32];
       tc::ld_16x256b_x8(((uint32_t)(32 * qd) << 16) + T_SC, x);
@@ -672,7 +674,7 @@ __device__ void score_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
       const int r = it.rows(chunk_at(it, back, c));
       if (r < C) zero_rows<D>(sm.stage[k % NST][2], r, tid, 128);      // values behind the sequence's end, as the keys
       make_p(x, pz + C, back ? -1 : 1, r, qd, lane);
-      if (k > 0 && !(ok = wait_all(t, &sm.op_full, (uint32_t)((k - 1) & 1)))) break;     // the last P has been used
+      if (k > 0 && !(ok = wait_all(sm, &sm.op_full, (uint32_t)((k - 1) & 1)))) break;     // the last P has been used
       tc::fence_after_sync();
       // matrices: (rows 0-7, block y), (rows 8-15, block y), (rows 0-7, block y + 1), (rows 8-15, block y + 1)
       const uint32_t row = 16 * qd + (lane & 15), to = smem_addr(sm.p) + row * 128;
@@ -709,7 +711,7 @@ __device__ void out_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& sm, in
     for (int c = 0; c < it.chunks(); ++c, ++k) {
       const int ch = chunk_at(it, w.back, c), r = it.rows(ch), row = it.begin + ch * C;
       if (lane == 0) tc::bulk_wait_read_all();     // the last tile's store has left the buffer
-      if (!(ok = wait_all(t, &sm.op_full, (uint32_t)(k & 1)))) break;
+      if (!(ok = wait_all(sm, &sm.op_full, (uint32_t)(k & 1)))) break;
       tc::fence_after_sync();
       auto read = [&] {
         tc::fence_before_sync();
@@ -811,7 +813,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   float S[HC];
   StateIo last_io = {false, false, false, false};
   auto exchange = [&](bool swap, bool get, bool put) {
-    if (!wait_all(t, &sm.st_full[half], round++ & 1u)) return false;
+    if (!wait_all(sm, &sm.st_full[half], round++ & 1u)) return false;
     if (mine) exchange_state<D>(S, sm.st, e, swap, get, put);
     fence_proxy_async_smem();
     __syncwarp();
@@ -867,7 +869,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
 #pragma unroll
         for (int j = 0; j < HC; ++j) asm volatile("" : "+f"(S[j]));
       }
-      if (!(ok = wait_all(t, &sm.u_full[buffer_of<STATE_ONLY>(k)], phase_of<STATE_ONLY>(k)))) break;
+      if (!(ok = wait_all(sm, &sm.u_full[buffer_of<STATE_ONLY>(k)], phase_of<STATE_ONLY>(k)))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int j0 = 0; j0 < HC; j0 += 16) {
@@ -892,7 +894,7 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
         }
       }
       if (STATE_ONLY) continue;
-      if (!(ok = wait_all(t, &sm.op_full, par))) break;          // the last copy has been used
+      if (!(ok = wait_all(sm, &sm.op_full, par))) break;          // the last copy has been used
       tc::fence_after_sync();
       if (c + 1 < it.chunks()) {
         if (mine) state_to_tmem<D>(S, lane_addr + T_S + (HC / 2) * half);
@@ -909,15 +911,17 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
 
 // A block in which a wait gave up leaves NaN in all that its items were to write, so that nobody takes what lies there for
 // results (a stretch's state hands them on to the stretches behind it).  Threads 0 .. 255 of the state's warps, when every
-// store of the block has completed.
+// store of the block has completed.  (Rolled loops: the kernel is short of room for instructions.)
 template <int D, bool STATE_ONLY>
 __device__ void spoil(const LinTc& t, const LinSmem<D>& sm, int thread) {
+#pragma unroll 1
   for (int i = 0; i < item_rounds(t); ++i) {
     const Item it = item_of<STATE_ONLY>(t, sm.order, i);
     if (!it.on) continue;
     const LinWalk& w = t.a.walk[it.w];
     if (!STATE_ONLY) {
       const int r0 = it.begin + it.c0 * C, rows = min(it.len - it.c0 * C, (it.c1 - it.c0) * C);
+#pragma unroll 1
       for (int64_t x = thread; x < (int64_t)rows * (D / 8); x += 256) {
         uint16_t* dst = reinterpret_cast<uint16_t*>(w.out) + (r0 + x / (D / 8)) * w.out_stride + it.h * D + 8 * (x % (D / 8));
         *reinterpret_cast<uint4*>(dst) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
@@ -926,6 +930,7 @@ __device__ void spoil(const LinTc& t, const LinSmem<D>& sm, int thread) {
     if (state_io<STATE_ONLY>(t, it).out) {
       float* S = STATE_ONLY ? t.ws + stretch_index(t.a, t.split, it.w, it.n, it.h, it.seg) * (D * D)
                             : w.S_out + ((int64_t)it.n * t.a.H + it.h) * (D * D);
+#pragma unroll 1
       for (int x = thread; x < D * D; x += 256) S[x] = __int_as_float(0x7fffffff);
     }
   }
@@ -961,6 +966,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&sm.drain[1], 1);
     mbar_init(&sm.sc_empty, 4);
     sm.bad = 0;
+    sm.tries = t.tries;
     fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(&sm.taddr, 512);
