@@ -413,6 +413,7 @@ def _plain(name: str, t: Optional[torch.Tensor], shape, dtype, like: torch.Tenso
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # current_stream() without the wrapper object
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)     # current_device() likewise
 
 
 class _On:
@@ -439,7 +440,7 @@ class _On:
 
 def _run(name: str, fn, index: int, stream, *args) -> None:
     """fn(*args, stream) with device `index` current."""
-    if stream is None and _raw_stream is not None and torch.cuda.current_device() == index:
+    if stream is None and _raw_stream is not None and _device_now() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with _On(index, stream) as st:
@@ -465,6 +466,8 @@ def _whole(name: str, x) -> Optional[int]:
 
 def _number(name: str, x) -> float:
     """A real number as a float."""
+    if type(x) is float:
+        return x
     try:
         return float(x)
     except (TypeError, ValueError, RuntimeError):
@@ -475,7 +478,7 @@ def _form(t):
     if t is None:
         return None
     try:
-        return t.shape, t.stride(), t.dtype, t.get_device()
+        return t.shape, t.stride(), t.dtype, t.get_device(), t.requires_grad
     except AttributeError:
         return type(t)                           # no tensor: the checks of a first call refuse it
 
@@ -490,14 +493,16 @@ def _plan(key, build):
     return plan
 
 
-def _detached(name: str, *tensors) -> None:
+def _wants_grad(*tensors) -> bool:
+    """Of a plan's inputs: whether one requires gradients."""
+    return any(t is not None and t.requires_grad for t in tensors)
+
+
+def _detached(name: str) -> None:
     """Says so where autograd would be expected to record the call: the outputs are detached."""
     if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                warnings.warn(f"{name} records nothing for autograd, its outputs are detached from inputs that require gradients: "
-                              f"call it in an autograd function (or under torch.no_grad())", stacklevel=3)
-                return
+        warnings.warn(f"{name} records nothing for autograd, its outputs are detached from inputs that require gradients: "
+                      f"call it in an autograd function (or under torch.no_grad())", stacklevel=3)
 
 
 def _opt(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -597,17 +602,19 @@ def pace_linattn_forward(q, k, v, log_decay, o=None, ST=None, num_seqs=None, max
         _plain("S0", S0, (n, H, d, d), torch.float32, q)
         _plain("ST", ST, (n, H, d, d), torch.float32, q)
         _plain("flags", flags, (1,), torch.int32, q)
-        return desc, ctypes.byref(desc), (n, H, d, d), _lin_workspace("pace_linattn_forward", desc, 0)
+        return (desc, ctypes.byref(desc), (n, H, d, d), _lin_workspace("pace_linattn_forward", desc, 0),
+                _wants_grad(q, k, v, log_decay, S0))
 
-    desc, ref, states, size = _plan(("fwd", _form(q), _form(k), _form(v), _form(log_decay), _form(o), _form(ST),
+    _, ref, states, size, grads = _plan(("fwd", _form(q), _form(k), _form(v), _form(log_decay), _form(o), _form(ST),
                                      _form(cu_seqlens), _form(S0), _form(flags), num_seqs, max_len), build)
-    _detached("pace_linattn_forward", q, k, v, log_decay, S0)
+    if grads:
+        _detached("pace_linattn_forward")
     if o is None:
         o = _like(q, stream)
     if ST is None and need_ST:
         ST = _new(states, torch.float32, q, stream) if S0 is None else _like(S0, stream)
     ws = _workspace("pace_linattn_forward", size, workspace, q, stream)
-    _run("pace_linattn_forward", lib.pace_linattn_forward, q.device.index, stream, ref, q.data_ptr(), k.data_ptr(),
+    _run("pace_linattn_forward", lib.pace_linattn_forward, q.get_device(), stream, ref, q.data_ptr(), k.data_ptr(),
          v.data_ptr(), log_decay.data_ptr(), _opt(cu_seqlens), _opt(S0), o.data_ptr(), _opt(ST), _opt(ws), _opt(flags))
     return o, ST
 
@@ -638,12 +645,14 @@ def pace_linattn_backward(q, k, v, log_decay, d_o, dq=None, dk=None, dv=None, dS
         _plain("dST", dST, (n, H, d, d), torch.float32, q)
         _plain("dS0", dS0, (n, H, d, d), torch.float32, q)
         _plain("flags", flags, (1,), torch.int32, q)
-        return desc, ctypes.byref(desc), (n, H, d, d), rooms, _lin_workspace("pace_linattn_backward", desc, 1)
+        return (desc, ctypes.byref(desc), (n, H, d, d), rooms, _lin_workspace("pace_linattn_backward", desc, 1),
+                _wants_grad(q, k, v, log_decay, S0, d_o, dST))
 
-    desc, ref, states, rooms, size = _plan(
+    _, ref, states, rooms, size, grads = _plan(
         ("bwd", _form(q), _form(k), _form(v), _form(log_decay), _form(d_o), _form(dq), _form(dk), _form(dv), _form(dS0),
          _form(cu_seqlens), _form(S0), _form(dST), _form(flags), num_seqs, max_len), build)
-    _detached("pace_linattn_backward", q, k, v, log_decay, S0, d_o, dST)
+    if grads:
+        _detached("pace_linattn_backward")
     made = []
     for given, like, room in ((dq, q, rooms[0]), (dk, k, rooms[1]), (dv, v, rooms[2])):
         if given is None:
@@ -654,7 +663,7 @@ def pace_linattn_backward(q, k, v, log_decay, d_o, dq=None, dk=None, dv=None, dS
     if dS0 is None and (S0 is not None if need_dS0 is None else need_dS0):
         dS0 = _new(states, torch.float32, q, stream)
     ws = _workspace("pace_linattn_backward", size, workspace, q, stream)
-    _run("pace_linattn_backward", lib.pace_linattn_backward, q.device.index, stream, ref, q.data_ptr(), k.data_ptr(),
+    _run("pace_linattn_backward", lib.pace_linattn_backward, q.get_device(), stream, ref, q.data_ptr(), k.data_ptr(),
          v.data_ptr(), log_decay.data_ptr(), _opt(cu_seqlens), _opt(S0), d_o.data_ptr(), _opt(dST), dq.data_ptr(),
          dk.data_ptr(), dv.data_ptr(), _opt(dS0), _opt(ws), _opt(flags))
     return dq, dk, dv, dS0
@@ -677,13 +686,14 @@ def pace_linattn_step(S, q, k, v, log_decay, o=None, stream=None) -> torch.Tenso
         _plain("S", S, (n, H, d, d), torch.float32, q)
         _plain("log_decay", log_decay, (H,), torch.float32, q)
         desc = _LinattnDesc(n, H, d, d, _IO_OF[q.dtype], 0, 0, *strides)
-        return desc, ctypes.byref(desc)
+        return desc, ctypes.byref(desc), _wants_grad(S, q, k, v, log_decay)
 
-    _, ref = _plan(("step", _form(S), _form(q), _form(k), _form(v), _form(log_decay), _form(o)), build)
-    _detached("pace_linattn_step", S, q, k, v, log_decay)
+    _, ref, grads = _plan(("step", _form(S), _form(q), _form(k), _form(v), _form(log_decay), _form(o)), build)
+    if grads:
+        _detached("pace_linattn_step")
     if o is None:
         o = _like(q, stream)
-    _run("pace_linattn_step", lib.pace_linattn_step, q.device.index, stream, ref, S.data_ptr(), q.data_ptr(), k.data_ptr(),
+    _run("pace_linattn_step", lib.pace_linattn_step, q.get_device(), stream, ref, S.data_ptr(), q.data_ptr(), k.data_ptr(),
          v.data_ptr(), log_decay.data_ptr(), o.data_ptr())
     return o
 
@@ -754,16 +764,17 @@ def pace_qk_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_
                 desc.k_out_stride = st
             else:
                 desc.q_out_stride = st
-        return desc, ctypes.byref(desc)
+        return desc, ctypes.byref(desc), _wants_grad(q, k, q_weight, k_weight)
 
-    _, ref = _plan(("norm", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq),
+    _, ref, grads = _plan(("norm", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq),
                     _form(q_out), _form(k_out), rotary_dim, interleaved, norm, eps, q_scale), build)
-    _detached("pace_qk_norm_rotate", q, k, q_weight, k_weight)
+    if grads:
+        _detached("pace_qk_norm_rotate")
     if q_out is None and q is not None:
         q_out = _like(q, stream)
     if k_out is None and k is not None:
         k_out = _like(k, stream)
-    _run("pace_qk_norm_rotate", lib.pace_qk_norm_rotate, (k if q is None else q).device.index, stream, ref, _opt(q), _opt(k),
+    _run("pace_qk_norm_rotate", lib.pace_qk_norm_rotate, (k if q is None else q).get_device(), stream, ref, _opt(q), _opt(k),
          _opt(q_weight), _opt(k_weight), _opt(positions), _opt(inv_freq), _opt(q_out), _opt(k_out))
     return q_out, k_out
 
@@ -807,13 +818,14 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
             _plain(f"d{name}_weight", dw, (d,), torch.float32, like)
         size = ctypes.c_size_t()
         _check("pace_qk_norm_rotate_backward", lib.pace_qk_norm_workspace_bytes(ctypes.byref(desc), ctypes.byref(size)))
-        return desc, ctypes.byref(desc), size.value
+        return desc, ctypes.byref(desc), size.value, _wants_grad(q, k, q_weight, k_weight, d_q_out, d_k_out)
 
-    _, ref, size = _plan(
+    _, ref, size, grads = _plan(
         ("normb", _form(q), _form(k), _form(q_weight), _form(k_weight), _form(positions), _form(inv_freq), _form(d_q_out),
          _form(d_k_out), _form(dq), _form(dk), _form(dq_weight), _form(dk_weight), rotary_dim, interleaved, norm, eps,
          q_scale), build)
-    _detached("pace_qk_norm_rotate_backward", q, k, q_weight, k_weight, d_q_out, d_k_out)
+    if grads:
+        _detached("pace_qk_norm_rotate_backward")
     like = q if q is not None else k
     if dq is None and q is not None:
         dq = _like(q, stream)
@@ -826,7 +838,7 @@ def pace_qk_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, 
     ws = None
     if dq_weight is not None or dk_weight is not None:
         ws = _workspace("pace_qk_norm_rotate_backward", size, workspace, like, stream)
-    _run("pace_qk_norm_rotate_backward", lib.pace_qk_norm_rotate_backward, like.device.index, stream, ref, _opt(q), _opt(k),
+    _run("pace_qk_norm_rotate_backward", lib.pace_qk_norm_rotate_backward, like.get_device(), stream, ref, _opt(q), _opt(k),
          _opt(q_weight), _opt(k_weight), _opt(positions), _opt(inv_freq), _opt(d_q_out), _opt(d_k_out), _opt(dq), _opt(dk),
          _opt(dq_weight), _opt(dk_weight), _opt(ws))
     return dq, dk, dq_weight, dk_weight
