@@ -28,7 +28,8 @@ constexpr unsigned FULL = 0xffffffffu;
 // that it is only for products value key^T above 1e31 that S could overflow.
 //
 // 8 sequences x 16 heads, 1000 tokens, d = 64, fp32: 124 us; 16 x 32 heads, 512 tokens: 177 us, where reads of shared
-// memory and shuffles keep L1 85 % busy (the packed products their pipe 48 %); with fewer heads it is latency.
+// memory and shuffles keep L1 85 % busy (the packed products have 29 % of their pipe's instruction slots, two each); with
+// fewer heads it is latency.
 constexpr int kWalkThreads = 128, kRows = 32, TT = 16;
 
 template <int D>

@@ -33,10 +33,12 @@
 // without outputs gives each stretch's own contribution to the state, a small
 // one chains them, and the stretches then run from their true states.
 //
-// Gradients of 8 x 32 heads, 4096 tokens, d = 128: 887 us (0.32 of the measured copy); 64 prompts of 1 to 1021 tokens, 32
-// heads, with states: 235 us (0.40); one of 65536 tokens, 32 heads: 465 us (0.35).  A chunk takes about 3800 cycles,
-// of which its products alone would take 1700; the rest is what the groups wait for one another.  Long runs draw 1000 W,
-// which holds the SM clock at 1.5 to 1.75 GHz.
+// Gradients of 8 x 32 heads, 4096 tokens, d = 128: 909 us (0.32 of the measured copy); 64 prompts of 1 to 1021 tokens, 32
+// heads, with states: 239 us (0.40); one of 32768 tokens, 32 heads: 471 us (0.35).  In the steady state a chunk takes 4000
+// cycles (d = 64: 3300), of a backward pass 3500 (3100), and the tensor pipe is active for 30 % of them; the rest is what
+// the groups wait for one another and, a fifth of it, for instructions: the loops fill the instruction cache, so that code
+// costs time even where it is not run.  Loops of seconds over long sequences draw 995 W, which holds the SM clock at 1.5 to
+// 1.8 GHz (the ragged prompts 910 W, at the full clock).
 #include <atomic>
 
 #include "linattn_tc.cuh"
