@@ -773,21 +773,22 @@ __device__ __forceinline__ void state_to_tmem(const float (&S)[D / 2], uint32_t 
   ltc::wait_st();
 }
 
-// This thread's part of the state (row e of its half of the key channels) out of shared memory, into it, or exchanged.
+// This thread's part of the state (row e of its half of the key channels) exchanged for what lies in shared memory.  Both ways
+// in every case: where one is not wanted, what is read is not used, or what is written not stored; a choice made this code,
+// unrolled over the registers that hold the state, a third of the kernel's.
 // Rows of 128 bytes whose 16-byte pieces are exchanged by the row's low bits: the lanes of a row-wise access fall in
 // distinct banks, as those of a column-wise one (`swap`: the state lies transposed) do anyway.
 template <int D>
-__device__ __forceinline__ void exchange_state(float (&S)[D / 2], uint8_t* st, int e, bool swap, bool get, bool put) {
+__device__ __forceinline__ void exchange_state(float (&S)[D / 2], uint8_t* st, int e, bool swap) {
   constexpr int HC = D / 2;
   if (!swap) {
     uint8_t* row = st + e * 128;
 #pragma unroll
     for (int j = 0; j < HC; j += 4) {
       float4* at = reinterpret_cast<float4*>(row + (j / 32) * (D * 128) + ((((j % 32) / 4) ^ (e & 7)) << 4));
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (get) x = *at;
-      if (put) *at = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-      if (get || put) S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
+      const float4 x = *at;
+      *at = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
     }
   } else {
     uint8_t* col = st + (e >> 5) * (D * 64) + (e & 3) * 4;
@@ -795,10 +796,9 @@ __device__ __forceinline__ void exchange_state(float (&S)[D / 2], uint8_t* st, i
 #pragma unroll
     for (int j = 0; j < HC; ++j) {
       float* at = reinterpret_cast<float*>(col + j * 128 + ((piece ^ (j & 7)) << 4));
-      float x = 0.f;
-      if (get) x = *at;
-      if (put) *at = S[j];
-      if (get || put) S[j] = x;
+      const float x = *at;
+      *at = S[j];
+      S[j] = x;
     }
   }
 }
@@ -814,25 +814,27 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
   bool ok = true;
   float S[HC];
   StateIo last_io = {false, false, false, false};
-  auto exchange = [&](bool swap, bool get, bool put) {
-    if (!wait_all(sm, &sm.st_full[half], round++ & 1u)) return false;
-    if (mine) exchange_state<D>(S, sm.st, e, swap, get, put);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&sm.st_done[half]);
-    return true;
-  };
-  for (int i = 0; i < item_rounds(t); ++i) {
+#pragma unroll
+  for (int j = 0; j < HC; ++j) S[j] = 0.f;
+  // one round more than there are items: the last one's state goes out
+#pragma unroll 1
+  for (int i = 0; i <= item_rounds(t); ++i) {
+    const bool end = i == item_rounds(t);
+    if (end && !last_io.out) break;
     const Item it = item_of<STATE_ONLY>(t, sm.order, i);
-    if (!it.on) continue;
-    const StateIo io = state_io<STATE_ONLY>(t, it);
-    const bool back = t.a.walk[it.w].back;
-    if (two_rounds(last_io, io)) {
-      if (!(ok = exchange(last_io.out_swap, false, true))) break;
-      if (!(ok = exchange(io.in_swap, true, false))) break;
-    } else if (!(ok = exchange(io.in ? io.in_swap : last_io.out_swap, io.in, last_io.out))) {
-      break;
+    if (!it.on && !end) continue;
+    StateIo io = {false, false, false, false};
+    if (!end) io = state_io<STATE_ONLY>(t, it);
+    const bool back = t.a.walk[it.w].back, two = two_rounds(last_io, io);
+#pragma unroll 1
+    for (int turn = two ? 0 : 1; turn < 2; ++turn) {
+      if (!(ok = wait_all(sm, &sm.st_full[half], round++ & 1u))) break;
+      if (mine && (io.in || last_io.out)) exchange_state<D>(S, sm.st, e, turn && io.in ? io.in_swap : last_io.out_swap);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.st_done[half]);
     }
+    if (end || !ok) break;
     last_io = io;
     if (!io.in) {
 #pragma unroll
@@ -907,7 +909,6 @@ __device__ void state_role(const LinTc& t, LinSmem<D>& sm, int warp, int lane) {
     }
     if (!ok) break;
   }
-  if (ok && last_io.out) ok = exchange(last_io.out_swap, false, true);
   if (!ok) gave_up(t, sm);
 }
 
