@@ -312,6 +312,7 @@ __device__ void state_io_role(const LinTc& t, const LinMaps& maps, LinSmem<D>& s
 template <int D, bool STATE_ONLY>
 __device__ __forceinline__ int chunks_of_block(const LinTc& t, const LinSmem<D>& sm) {
   int total = 0;
+#pragma unroll 1
   for (int i = 0; i < item_rounds(t); ++i) total += item_of<STATE_ONLY>(t, sm.order, i).chunks();
   return total;
 }
