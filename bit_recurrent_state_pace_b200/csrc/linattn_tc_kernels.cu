@@ -33,12 +33,12 @@
 // without outputs gives each stretch's own contribution to the state, a small
 // one chains them, and the stretches then run from their true states.
 //
-// Gradients of 8 x 32 heads, 4096 tokens, d = 128: 909 us (0.32 of the measured copy); 64 prompts of 1 to 1021 tokens, 32
-// heads, with states: 239 us (0.40); one of 32768 tokens, 32 heads: 471 us (0.35).  In the steady state a chunk takes 4000
-// cycles (d = 64: 3300), of a backward pass 3500 (3100), and the tensor pipe is active for 30 % of them; the rest is what
+// Gradients of 8 x 32 heads, 4096 tokens, d = 128: 857 us (0.33 of the measured copy); 64 prompts of 1 to 1021 tokens, 32
+// heads, with states: 228 us (0.42); one of 32768 tokens, 32 heads: 478 us (0.34).  In the steady state a chunk takes 4200
+// cycles (d = 64: 3400), of a backward pass 3600 (3400), and the tensor pipe is active for 30 % of them; the rest is what
 // the groups wait for one another and, a fifth of it, for instructions: the loops fill the instruction cache, so that code
-// costs time even where it is not run.  Loops of seconds over long sequences draw 995 W, which holds the SM clock at 1.5 to
-// 1.8 GHz (the ragged prompts 910 W, at the full clock).
+// costs time even where it is not run.  Loops of seconds over long sequences draw 990 W, which holds the SM clock at 1.55 to
+// 1.8 GHz (the ragged prompts 950 W, at the full clock).
 #include <atomic>
 
 #include "linattn_tc.cuh"
@@ -776,7 +776,7 @@ __device__ __forceinline__ void state_to_tmem(const float (&S)[D / 2], uint32_t 
 
 // This thread's part of the state (row e of its half of the key channels) exchanged for what lies in shared memory.  Both ways
 // in every case: where one is not wanted, what is read is not used, or what is written not stored; a choice made this code,
-// unrolled over the registers that hold the state, a third of the kernel's.
+// unrolled over the registers that hold the state, a third of the kernel's (training gradients 878 us, so 783).
 // Rows of 128 bytes whose 16-byte pieces are exchanged by the row's low bits: the lanes of a row-wise access fall in
 // distinct banks, as those of a column-wise one (`swap`: the state lies transposed) do anyway.
 template <int D>
